@@ -25,6 +25,8 @@ __all__ = [
     "rc_all_reduce", "rc_reduce_scatter", "rc_all_gather", "rc_reduce", "rc_broadcast",
     "rc_ring_all_reduce", "rc_ring_all_reduce_noalloc", "rc_hier_all_reduce", "rc_copy", "rc_reserve_workspace", "rc_workspace_bytes", "rc_check_buffer",
     "rc_probe_bounded_wait",
+    "rc_dropout", "rc_all_reduce_dropout", "rc_moe_gate", "rc_moe_gate_backward", "rc_moe_gate_workspace",
+    "rc_vocab_ce_forward", "rc_vocab_ce_backward", "rc_vocab_ce_workspace",
     "rc_rank_all_reduce", "rc_rank_reduce_scatter", "rc_rank_all_gather", "rc_rank_ring_step",
     "rc_ipc_handle", "rc_ipc_export", "rc_ipc_import", "rc_ipc_release",
     "rc_stream_status", "rc_launch_count", "rc_finalize", "rc_version", "rc_last_error",
@@ -89,6 +91,15 @@ _decl("rc_bucketer_ready", [_vp, _i, _vp])
 _decl("rc_bucketer_flush", [_vp, _vp])
 _decl("rc_bucketer_destroy", [_vp])
 _decl("rc_all_to_all_v", [_vpp, _vpp, _i, ctypes.POINTER(ctypes.c_size_t), _i, _vp])
+_d, _u64, _i32 = ctypes.c_double, ctypes.c_uint64, ctypes.c_int32
+_decl("rc_dropout", [_vpp, _vpp, _vpp, _i, _sz, _i, _f, _d, _u64, _u64, _u64, _vp])
+_decl("rc_all_reduce_dropout", [_vpp, _vpp, _vpp, _i, _sz, _i, _f, _d, _u64, _u64, _vp])
+_decl("rc_moe_gate_workspace", [_i, _i, _szp])
+_decl("rc_moe_gate", [_vpp, _vpp, _vpp, _vpp, _vpp, _vp, _vp, _i, _sz, _i, _i, _i, _i, _f, _vp, _sz, _vp])
+_decl("rc_moe_gate_backward", [_vpp, _vpp, _vpp, _vpp, _vp, _vp, _vpp, _i, _sz, _i, _i, _i, _i, _f, _vp])
+_decl("rc_vocab_ce_workspace", [_sz, _sz, _sz, _i, _i, _i, _i, _szp])
+_decl("rc_vocab_ce_forward", [_vp, _vpp, _vp, _vp, _vp, _sz, _sz, _sz, _i, _i, _i32, _vp, _sz, _vp])
+_decl("rc_vocab_ce_backward", [_vp, _vpp, _vp, _vp, _vp, _vp, _vpp, _sz, _sz, _sz, _i, _i, _i32, _vp, _sz, _vp])
 _decl("rc_rank_all_reduce", [_vpp, _vpp, _i, _i, _sz, _i, _i, _f, _vp])
 _decl("rc_rank_reduce_scatter", [_vpp, _vp, _i, _i, _sz, _i, _i, _i, _f, _vp])
 _decl("rc_rank_all_gather", [_vpp, _vp, _i, _i, _sz, _i, _vp])
@@ -421,6 +432,209 @@ class Bucketer:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- training-step operators
+def _opt_ptrs(xs):
+    return None if xs is None else _ptrs(xs)
+
+
+def _same_len(p: int, **lists) -> None:
+    for name, xs in lists.items():
+        if xs is not None and len(xs) != p:
+            raise ValueError(f"{name} holds {len(xs)} buffers for {p} ranks")
+
+
+def _want(x, dtype: str, shape, what: str) -> None:
+    """A tensor's element type and shape (raw addresses are the caller's)."""
+    if x is None or not _is_tensor(x):
+        return
+    if str(x.dtype) not in ("torch." + dtype, "torch.bool" if dtype == "uint8" else ""):
+        raise TypeError(f"{what} must be {dtype}, not {x.dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+
+
+def _float_name(dt: int) -> str:
+    return {FP32: "float32", BF16: "bfloat16"}.get(dt, "float32")
+
+
+def _workspace(ws, nbytes: int, stream):
+    """(address, bytes, owner): the caller's workspace, or one from torch's
+    allocator that the stream's pending work keeps."""
+    if ws is not None:
+        if not _is_tensor(ws):
+            raise TypeError("workspace must be a CUDA tensor")
+        return _addr(ws), ws.numel() * ws.element_size(), ws
+    import torch
+    ws = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device="cuda")
+    s = _stream(stream)
+    if s != torch.cuda.current_stream().cuda_stream:
+        # the block may be handed on only after the work on that stream
+        ext = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+        ext.wait_stream(torch.cuda.current_stream())
+        ws.record_stream(ext)
+    return ws.data_ptr(), ws.numel(), ws
+
+
+def rc_dropout(send: Sequence[Buf], recv: Sequence[Buf], prob: float, seed: int, offset: int = 0, rank_stride: int = 0,
+               residual: Optional[Sequence[Buf]] = None, n=None, dtype=None, scale=1.0, stream=None):
+    """recv[r] = residual[r] + dropout(scale * send[r]); the mask follows from
+    seed and the index offset + r * rank_stride + i (see the header)."""
+    p = len(send)
+    _same_len(p, recv=recv, residual=residual)
+    _check(lib.rc_dropout(_ptrs(send), _opt_ptrs(residual), _ptrs(recv), p, _numel(send[0], n), _dt(dtype, send[0]),
+                          scale, prob, int(seed), int(offset), int(rank_stride), _stream(stream)), "rc_dropout")
+
+
+def rc_all_reduce_dropout(send: Sequence[Buf], recv: Sequence[Buf], prob: float, seed: int, offset: int = 0,
+                          residual: Optional[Sequence[Buf]] = None, n=None, dtype=None, scale=1.0, stream=None):
+    """recv[r] = residual[r] + dropout(scale * sum over the ranks of send), one
+    mask for all ranks.  Its backward is rc_dropout with rank_stride 0."""
+    p = len(send)
+    _same_len(p, recv=recv, residual=residual)
+    _check(lib.rc_all_reduce_dropout(_ptrs(send), _opt_ptrs(residual), _ptrs(recv), p, _numel(send[0], n),
+                                     _dt(dtype, send[0]), scale, prob, int(seed), int(offset), _stream(stream)),
+           "rc_all_reduce_dropout")
+
+
+def rc_moe_gate_workspace(tokens: int, experts: int, p: int) -> int:
+    """Bytes of workspace rc_moe_gate needs on the current device (for any number of tokens)."""
+    out = ctypes.c_size_t()
+    _check(lib.rc_moe_gate_workspace(p, int(experts), ctypes.byref(out)), "rc_moe_gate_workspace")
+    return out.value
+
+
+def _gate_sizes(logits, ids, tokens, experts, top_k):
+    if tokens is None or experts is None:
+        if not _is_tensor(logits[0]):
+            raise ValueError("tokens and experts are required when buffers are raw addresses")
+        tokens, experts = logits[0].shape
+    if top_k is None:
+        if not _is_tensor(ids[0]):
+            raise ValueError("top_k is required when ids are raw addresses")
+        top_k = ids[0].shape[1]
+    return int(tokens), int(experts), int(top_k)
+
+
+def rc_moe_gate(logits: Sequence[Buf], ids: Sequence[Buf], weights: Sequence[Buf], counts: Sequence[Buf], stats: Buf,
+                loss: Buf, token_mask: Optional[Sequence[Buf]] = None, normalize: bool = True, coef: float = 0.01,
+                workspace=None, tokens=None, experts=None, top_k=None, dtype=None, stream=None):
+    """Top-k experts of every token, their weights, per-rank counts, and the
+    balance loss over all ranks.  logits[r] is [tokens, experts], ids[r]
+    (int32) and weights[r] (float32) [tokens, top_k], counts[r] (int32)
+    [experts], stats 2 * experts + 1 floats, loss one float."""
+    p = len(logits)
+    _same_len(p, ids=ids, weights=weights, counts=counts, token_mask=token_mask)
+    t, e, k = _gate_sizes(logits, ids, tokens, experts, top_k)
+    dt = _dt(dtype, logits[0])
+    for r in range(p):
+        _want(logits[r], _float_name(dt), (t, e), f"logits[{r}]")
+        _want(ids[r], "int32", (t, k), f"ids[{r}]")
+        _want(weights[r], "float32", (t, k), f"weights[{r}]")
+        _want(counts[r], "int32", (e,), f"counts[{r}]")
+        if token_mask is not None:
+            _want(token_mask[r], "uint8", (t,), f"token_mask[{r}]")
+    _want(stats, "float32", (2 * e + 1,), "stats")
+    _want(loss, "float32", None, "loss")
+    need = 0 if workspace is not None else rc_moe_gate_workspace(t, e, p)
+    ws, nbytes, _keep = _workspace(workspace, need, stream)
+    _check(lib.rc_moe_gate(_ptrs(logits), _opt_ptrs(token_mask), _ptrs(ids), _ptrs(weights), _ptrs(counts),
+                           _addr(stats), _addr(loss), p, t, e, k, dt, int(bool(normalize)), coef, ws, nbytes,
+                           _stream(stream)), "rc_moe_gate")
+
+
+def rc_moe_gate_backward(logits: Sequence[Buf], ids: Sequence[Buf], stats: Buf, dlogits: Sequence[Buf],
+                         dweights: Optional[Sequence[Buf]] = None, dloss: Optional[Buf] = None,
+                         token_mask: Optional[Sequence[Buf]] = None, normalize: bool = True, coef: float = 0.01,
+                         tokens=None, experts=None, top_k=None, dtype=None, stream=None):
+    """Gradient to the logits from dweights[r] ([tokens, top_k] float32) and
+    dloss (one float); ids and stats are rc_moe_gate's."""
+    p = len(logits)
+    _same_len(p, ids=ids, dlogits=dlogits, dweights=dweights, token_mask=token_mask)
+    t, e, k = _gate_sizes(logits, ids, tokens, experts, top_k)
+    dt = _dt(dtype, logits[0])
+    for r in range(p):
+        _want(logits[r], _float_name(dt), (t, e), f"logits[{r}]")
+        _want(dlogits[r], _float_name(dt), (t, e), f"dlogits[{r}]")
+        _want(ids[r], "int32", (t, k), f"ids[{r}]")
+        if dweights is not None:
+            _want(dweights[r], "float32", (t, k), f"dweights[{r}]")
+        if token_mask is not None:
+            _want(token_mask[r], "uint8", (t,), f"token_mask[{r}]")
+    _want(stats, "float32", (2 * e + 1,), "stats")
+    _want(dloss, "float32", None, "dloss")
+    _check(lib.rc_moe_gate_backward(_ptrs(logits), _opt_ptrs(token_mask), _ptrs(ids), _opt_ptrs(dweights), _addr(stats),
+                                    None if dloss is None else _addr(dloss), _ptrs(dlogits), p, t, e, k, dt,
+                                    int(bool(normalize)), coef, _stream(stream)), "rc_moe_gate_backward")
+
+
+def rc_vocab_ce_workspace(tokens: int, d: int, vocab: int, p: int, backward: bool = False, unaligned: bool = False,
+                          dtype="bf16") -> int:
+    """Bytes of workspace the forward call needs, and the backward call too
+    when `backward`; `unaligned`: hidden or a weight is not 16-byte aligned."""
+    out = ctypes.c_size_t()
+    _check(lib.rc_vocab_ce_workspace(int(tokens), int(d), int(vocab), p, _dt(dtype), int(bool(backward)),
+                                     int(bool(unaligned)), ctypes.byref(out)), "rc_vocab_ce_workspace")
+    return out.value
+
+
+def _ce_sizes(hidden, weight, tokens, d, vocab, dtype):
+    if tokens is None or d is None:
+        if not _is_tensor(hidden):
+            raise ValueError("tokens and d are required when buffers are raw addresses")
+        tokens, d = hidden.shape
+    if vocab is None:
+        if not all(_is_tensor(w) for w in weight):
+            raise ValueError("vocab is required when weights are raw addresses")
+        vocab = sum(w.shape[0] for w in weight)
+    p, dt = len(weight), _dt(dtype, hidden)
+    c = -(-int(vocab) // p)
+    rows = [max(0, min(int(vocab), (r + 1) * c) - r * c) for r in range(p)]
+    _want(hidden, _float_name(dt), (tokens, d), "hidden")
+    for r, w in enumerate(weight):
+        _want(w, _float_name(dt), (rows[r], d), f"weight[{r}]")
+    return int(tokens), int(d), int(vocab), p, dt, rows
+
+
+def _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, backward, stream):
+    need = 0
+    if workspace is None:
+        unaligned = any(_addr(x) % 16 for x in [hidden, *weight])
+        need = rc_vocab_ce_workspace(t, d, v, p, backward, unaligned, dt)
+    return _workspace(workspace, need, stream)
+
+
+def rc_vocab_ce_forward(hidden: Buf, weight: Sequence[Buf], target: Buf, loss: Buf, lse: Buf, ignore_index: int = -100,
+                        workspace=None, tokens=None, d=None, vocab=None, dtype=None, stream=None):
+    """Cross entropy of every token over the ranks' vocabulary pieces:
+    hidden [tokens, d], weight[r] [rows, d] (bf16), target (int32) [tokens];
+    loss and lse (float32) [tokens] are written."""
+    t, d, v, p, dt, _ = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
+    _want(target, "int32", (t,), "target")
+    _want(loss, "float32", (t,), "loss")
+    _want(lse, "float32", (t,), "lse")
+    ws, nbytes, _keep = _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, False, stream)
+    _check(lib.rc_vocab_ce_forward(_addr(hidden), _ptrs(weight), _addr(target), _addr(loss), _addr(lse), t, d, v, p, dt,
+                                   int(ignore_index), ws, nbytes, _stream(stream)), "rc_vocab_ce_forward")
+
+
+def rc_vocab_ce_backward(hidden: Buf, weight: Sequence[Buf], target: Buf, lse: Buf, dloss: Buf, dhidden: Buf,
+                         dweight: Sequence[Buf], ignore_index: int = -100, workspace=None, tokens=None, d=None,
+                         vocab=None, dtype=None, stream=None):
+    """dhidden and dweight[r] from dloss (float32, [tokens]) and the forward's lse."""
+    t, d, v, p, dt, rows = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
+    _same_len(p, dweight=dweight)
+    _want(target, "int32", (t,), "target")
+    _want(lse, "float32", (t,), "lse")
+    _want(dloss, "float32", (t,), "dloss")
+    _want(dhidden, _float_name(dt), (t, d), "dhidden")
+    for r, w in enumerate(dweight):
+        _want(w, _float_name(dt), (rows[r], d), f"dweight[{r}]")
+    ws, nbytes, _keep = _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, True, stream)
+    _check(lib.rc_vocab_ce_backward(_addr(hidden), _ptrs(weight), _addr(target), _addr(lse), _addr(dloss),
+                                    _addr(dhidden), _ptrs(dweight), t, d, v, p, dt, int(ignore_index), ws, nbytes,
+                                    _stream(stream)), "rc_vocab_ce_backward")
 
 
 def rc_copy(src: Buf, dst: Buf, nbytes=None, stream=None):

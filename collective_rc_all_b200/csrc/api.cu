@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -817,6 +818,280 @@ rc_status rc_rank_ring_step(const void *const *send, void *const *recv, void *co
   return launched(launch_rank_ring_step(j, (cudaStream_t)stream), "rank ring step launch");
 }
 
+// ---------------------------------------------------------------- training-step operators
+namespace {
+// Any buffer that must not overlap another one gets a rank id of its own.
+struct Distinct {
+  std::vector<Buf> bs;
+  int next = 1000;
+  void add(const void *ptr, uint64_t elems, int esz, bool out, const char *what, int idx) {
+    if (elems > 0) bs.push_back(make_buf(ptr, elems, esz, 0, next++, out, what, idx));
+  }
+};
+
+rc_status check_all(const std::vector<Buf> &bs) {
+  rc_status st = check_ranges(bs);
+  return st != RC_OK ? st : check_aliasing(bs);
+}
+
+rc_status dropout_call(const void *const *send, const void *const *residual, void *const *recv, int p, size_t n,
+                       rc_dtype dt, float scale, double prob, uint64_t seed, uint64_t offset, uint64_t rank_stride,
+                       bool reduce, rc_stream_t stream, const char *what) {
+  rc_status st;
+  if ((st = check_p_n(p, n)) != RC_OK) return st;
+  if (!float_dt_ok(dt)) return fail(RC_ERR_INVALID_ARG, "dtype must be fp32 or bf16");
+  if (!(prob >= 0.0 && prob <= 1.0)) return fail(RC_ERR_INVALID_ARG, "prob=%g outside [0, 1]", prob);
+  if (n == 0) return RC_OK;
+  if (!send || !recv) return fail(RC_ERR_INVALID_ARG, "pointer array is NULL");
+  const int s = dt_size(dt);
+  std::vector<Buf> bs;
+  for (int r = 0; r < p; ++r) bs.push_back(make_buf(send[r], n, s, 0, r, false, "send", r));
+  if (residual)
+    for (int r = 0; r < p; ++r) bs.push_back(make_buf(residual[r], n, s, 0, r, false, "residual", r));
+  for (int r = 0; r < p; ++r) bs.push_back(make_buf(recv[r], n, s, 0, r, true, "recv", r));
+  if ((st = check_all(bs)) != RC_OK) return st;
+  DropoutJob j{};
+  j.p = p;
+  j.n = n;
+  j.dt = dt;
+  j.seed = seed;
+  j.offset = offset;
+  j.rank_stride = rank_stride;
+  j.thr = (uint32_t)nearbyint(prob * 65536.0);
+  j.factor = j.thr < 65536u ? (float)((double)scale * (65536.0 / (65536.0 - (double)j.thr))) : 0.0f;
+  j.reduce = reduce;
+  for (int r = 0; r < p; ++r) {
+    j.x[r] = send[r];
+    j.res[r] = residual ? residual[r] : nullptr;
+    j.y[r] = recv[r];
+  }
+  return launched(launch_dropout(j, (cudaStream_t)stream), what);
+}
+
+rc_status check_gate(int p, size_t tokens, int experts, int top_k, rc_dtype dt) {
+  rc_status st;
+  if ((st = check_p_n(p, tokens)) != RC_OK) return st;
+  if (!float_dt_ok(dt)) return fail(RC_ERR_INVALID_ARG, "dtype must be fp32 or bf16");
+  if (experts < 1 || experts > 512) return fail(RC_ERR_INVALID_ARG, "experts=%d outside [1, 512]", experts);
+  if (top_k < 1 || top_k > 16 || top_k > experts)
+    return fail(RC_ERR_INVALID_ARG, "top_k=%d outside [1, min(16, experts=%d)]", top_k, experts);
+  if (tokens > 0x7fffffffull / (size_t)top_k)
+    return fail(RC_ERR_INVALID_ARG, "tokens=%zu x top_k=%d does not fit a 32-bit count", tokens, top_k);
+  return RC_OK;
+}
+
+rc_status check_workspace(Distinct *d, void *ws, size_t have, size_t need) {
+  if (have < need)
+    return fail(RC_ERR_INVALID_ARG, "workspace of %zu bytes is too small: %zu bytes are needed", have, need);
+  if ((uintptr_t)ws % 16 != 0) return fail(RC_ERR_INVALID_ARG, "workspace %p is not 16-byte aligned", ws);
+  d->add(ws, need, 1, true, "workspace", 0);
+  return RC_OK;
+}
+
+rc_status check_ce(size_t tokens, size_t d, size_t vocab, int p, rc_dtype dt) {
+  if (p < 1 || p > kMaxP) return fail(RC_ERR_INVALID_ARG, "p=%d outside [1, %d]", p, kMaxP);
+  if (dt == RC_FP32) return fail(RC_ERR_UNSUPPORTED, "the vocabulary cross entropy takes bf16 operands");
+  if (dt != RC_BF16) return fail(RC_ERR_INVALID_ARG, "dtype must be bf16");
+  constexpr size_t most = 0x7fffffffull - 4096;  // tile coordinates are 32-bit
+  if (tokens > most || vocab > most) return fail(RC_ERR_INVALID_ARG, "tokens=%zu or vocab=%zu too large", tokens, vocab);
+  if (d < 1 || d > (1u << 20)) return fail(RC_ERR_INVALID_ARG, "d=%zu outside [1, 1048576]", d);
+  if (vocab < 1) return fail(RC_ERR_INVALID_ARG, "vocab must be at least 1");
+  return RC_OK;
+}
+
+// Rows of rank r's vocabulary piece: the library's chunks of ceil(vocab / p).
+uint64_t ce_rows(size_t vocab, int p, int r) {
+  const uint64_t C = (vocab + p - 1) / p, lo = std::min<uint64_t>(vocab, C * r);
+  return std::min<uint64_t>(vocab, lo + C) - lo;
+}
+
+rc_status fill_ce(CeJob *j, const void *hidden, const void *const *weight, const int32_t *target, size_t tokens,
+                  size_t d, size_t vocab, int p, int32_t ignore_index, void *ws) {
+  if (!weight) return fail(RC_ERR_INVALID_ARG, "pointer array is NULL");
+  j->shape.tokens = (int64_t)tokens;
+  j->shape.vocab = (int64_t)vocab;
+  j->shape.d = (int)d;
+  j->shape.p = p;
+  j->hidden = hidden;
+  for (int r = 0; r < p; ++r) j->weight[r] = ce_rows(vocab, p, r) ? weight[r] : nullptr;
+  j->target = target;
+  j->ignore = ignore_index;
+  j->ws = ws;
+  return RC_OK;
+}
+}  // namespace
+
+rc_status rc_dropout(const void *const *send, const void *const *residual, void *const *recv, int p, size_t n,
+                     rc_dtype dt, float scale, double prob, uint64_t seed, uint64_t offset, uint64_t rank_stride,
+                     rc_stream_t stream) {
+  return dropout_call(send, residual, recv, p, n, dt, scale, prob, seed, offset, rank_stride, false, stream,
+                      "dropout launch");
+}
+
+rc_status rc_all_reduce_dropout(const void *const *send, const void *const *residual, void *const *recv, int p,
+                                size_t n, rc_dtype dt, float scale, double prob, uint64_t seed, uint64_t offset,
+                                rc_stream_t stream) {
+  return dropout_call(send, residual, recv, p, n, dt, scale, prob, seed, offset, 0, true, stream,
+                      "all_reduce_dropout launch");
+}
+
+rc_status rc_moe_gate_workspace(int p, int experts, size_t *bytes) {
+  if (!bytes) return fail(RC_ERR_INVALID_ARG, "output pointer is NULL");
+  rc_status st = check_gate(p, 0, experts, 1, RC_FP32);
+  if (st != RC_OK) return st;
+  *bytes = gate_workspace(p, experts);
+  return RC_OK;
+}
+
+rc_status rc_moe_gate(const void *const *logits, const uint8_t *const *token_mask, int32_t *const *ids,
+                      float *const *weights, int32_t *const *counts, float *stats, float *loss, int p, size_t tokens,
+                      int experts, int top_k, rc_dtype dt, int normalize, float coef, void *workspace,
+                      size_t workspace_bytes, rc_stream_t stream) {
+  rc_status st;
+  if ((st = check_gate(p, tokens, experts, top_k, dt)) != RC_OK) return st;
+  if (!logits || !ids || !weights || !counts) return fail(RC_ERR_INVALID_ARG, "pointer array is NULL");
+  Distinct b;
+  if ((st = check_workspace(&b, workspace, workspace_bytes, gate_workspace(p, experts))) != RC_OK) return st;
+  GateJob j{};
+  for (int r = 0; r < p; ++r) {
+    b.add(logits[r], tokens * experts, dt_size(dt), false, "logits", r);
+    if (token_mask) b.add(token_mask[r], tokens, 1, false, "token_mask", r);
+    b.add(ids[r], tokens * top_k, 4, true, "ids", r);
+    b.add(weights[r], tokens * top_k, 4, true, "weights", r);
+    b.add(counts[r], experts, 4, true, "counts", r);
+    j.logits[r] = logits[r];
+    j.mask[r] = token_mask ? token_mask[r] : nullptr;
+    j.ids[r] = ids[r];
+    j.weights[r] = weights[r];
+    j.counts[r] = counts[r];
+  }
+  b.add(stats, 2 * (uint64_t)experts + 1, 4, true, "stats", 0);
+  b.add(loss, 1, 4, true, "loss", 0);
+  if ((st = check_all(b.bs)) != RC_OK) return st;
+  j.stats = stats;
+  j.loss = loss;
+  j.ws = workspace;
+  j.p = p;
+  j.experts = experts;
+  j.top_k = top_k;
+  j.dt = dt;
+  j.tokens = tokens;
+  j.normalize = normalize != 0;
+  j.coef = coef;
+  return launched(launch_gate(j, (cudaStream_t)stream), "moe_gate launch");
+}
+
+rc_status rc_moe_gate_backward(const void *const *logits, const uint8_t *const *token_mask, const int32_t *const *ids,
+                               const float *const *dweights, const float *stats, const float *dloss,
+                               void *const *dlogits, int p, size_t tokens, int experts, int top_k, rc_dtype dt,
+                               int normalize, float coef, rc_stream_t stream) {
+  rc_status st;
+  if ((st = check_gate(p, tokens, experts, top_k, dt)) != RC_OK) return st;
+  if (tokens == 0) return RC_OK;
+  if (!logits || !ids || !dlogits) return fail(RC_ERR_INVALID_ARG, "pointer array is NULL");
+  Distinct b;
+  GateJob j{};
+  for (int r = 0; r < p; ++r) {
+    b.bs.push_back(make_buf(logits[r], tokens * experts, dt_size(dt), 0, r, false, "logits", r));
+    b.bs.push_back(make_buf(dlogits[r], tokens * experts, dt_size(dt), 0, r, true, "dlogits", r));
+    if (token_mask) b.add(token_mask[r], tokens, 1, false, "token_mask", r);
+    b.add(ids[r], tokens * top_k, 4, false, "ids", r);
+    if (dweights) b.add(dweights[r], tokens * top_k, 4, false, "dweights", r);
+    j.logits[r] = logits[r];
+    j.mask[r] = token_mask ? token_mask[r] : nullptr;
+    j.ids[r] = const_cast<int32_t *>(ids[r]);
+    j.dweights[r] = dweights ? dweights[r] : nullptr;
+    j.dlogits[r] = dlogits[r];
+  }
+  b.add(stats, 2 * (uint64_t)experts + 1, 4, false, "stats", 0);
+  if (dloss) b.add(dloss, 1, 4, false, "dloss", 0);
+  if ((st = check_all(b.bs)) != RC_OK) return st;
+  j.stats = const_cast<float *>(stats);
+  j.dloss = dloss;
+  j.p = p;
+  j.experts = experts;
+  j.top_k = top_k;
+  j.dt = dt;
+  j.tokens = tokens;
+  j.normalize = normalize != 0;
+  j.backward = true;
+  j.coef = coef;
+  return launched(launch_gate(j, (cudaStream_t)stream), "moe_gate_backward launch");
+}
+
+rc_status rc_vocab_ce_workspace(size_t tokens, size_t d, size_t vocab, int p, rc_dtype dt, int backward, int unaligned,
+                                size_t *bytes) {
+  rc_status st;
+  if (!bytes) return fail(RC_ERR_INVALID_ARG, "output pointer is NULL");
+  if ((st = check_ce(tokens, d, vocab, p, dt)) != RC_OK) return st;
+  *bytes = 0;
+  if (tokens == 0) return RC_OK;
+  CeShape s{(int64_t)tokens, (int64_t)vocab, (int)d, p};
+  const bool copies = unaligned || d % 8 != 0;
+  *bytes = ce_workspace(s, false, copies);
+  if (backward) *bytes = std::max(*bytes, ce_workspace(s, true, copies));
+  return RC_OK;
+}
+
+rc_status rc_vocab_ce_forward(const void *hidden, const void *const *weight, const int32_t *target, float *loss,
+                              float *lse, size_t tokens, size_t d, size_t vocab, int p, rc_dtype dt,
+                              int32_t ignore_index, void *workspace, size_t workspace_bytes, rc_stream_t stream) {
+  rc_status st;
+  if ((st = check_ce(tokens, d, vocab, p, dt)) != RC_OK) return st;
+  if (tokens == 0) return RC_OK;
+  CeJob j{};
+  if ((st = fill_ce(&j, hidden, weight, target, tokens, d, vocab, p, ignore_index, workspace)) != RC_OK) return st;
+  j.loss = loss;
+  j.lse = lse;
+  Distinct b;
+  if ((st = check_workspace(&b, workspace, workspace_bytes, ce_workspace(j))) != RC_OK) return st;
+  b.add(hidden, tokens * d, 2, false, "hidden", 0);
+  for (int r = 0; r < p; ++r) b.add(weight[r], ce_rows(vocab, p, r) * d, 2, false, "weight", r);
+  b.add(target, tokens, 4, false, "target", 0);
+  b.add(loss, tokens, 4, true, "loss", 0);
+  b.add(lse, tokens, 4, true, "lse", 0);
+  if ((st = check_all(b.bs)) != RC_OK) return st;
+  return launched(launch_ce_forward(j, (cudaStream_t)stream), "vocab_ce_forward launch");
+}
+
+rc_status rc_vocab_ce_backward(const void *hidden, const void *const *weight, const int32_t *target, const float *lse,
+                               const float *dloss, void *dhidden, void *const *dweight, size_t tokens, size_t d,
+                               size_t vocab, int p, rc_dtype dt, int32_t ignore_index, void *workspace,
+                               size_t workspace_bytes, rc_stream_t stream) {
+  rc_status st;
+  if ((st = check_ce(tokens, d, vocab, p, dt)) != RC_OK) return st;
+  if (!dweight) return fail(RC_ERR_INVALID_ARG, "pointer array is NULL");
+  CeJob j{};
+  Distinct b;
+  if ((st = fill_ce(&j, hidden, weight, target, tokens, d, vocab, p, ignore_index, workspace)) != RC_OK) return st;
+  j.lse_in = lse;
+  j.dloss = dloss;
+  j.dhidden = dhidden;
+  j.backward = true;
+  if (tokens > 0 && (st = check_workspace(&b, workspace, workspace_bytes, ce_workspace(j))) != RC_OK) return st;
+  b.add(hidden, tokens * d, 2, false, "hidden", 0);
+  b.add(dhidden, tokens * d, 2, true, "dhidden", 0);
+  for (int r = 0; r < p; ++r) {
+    j.dweight[r] = dweight[r];
+    b.add(weight[r], ce_rows(vocab, p, r) * d, 2, false, "weight", r);
+    b.add(dweight[r], ce_rows(vocab, p, r) * d, 2, true, "dweight", r);
+  }
+  b.add(target, tokens, 4, false, "target", 0);
+  b.add(lse, tokens, 4, false, "lse", 0);
+  b.add(dloss, tokens, 4, false, "dloss", 0);
+  if ((st = check_all(b.bs)) != RC_OK) return st;
+  if (tokens == 0) {  // no token: the weights' gradient is zero
+    for (int r = 0; r < p; ++r) {
+      const uint64_t bytes = ce_rows(vocab, p, r) * d * 2;
+      if (!bytes) continue;
+      cudaError_t e = cudaMemsetAsync(dweight[r], 0, bytes, (cudaStream_t)stream);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    }
+    return RC_OK;
+  }
+  return launched(launch_ce_backward(j, (cudaStream_t)stream), "vocab_ce_backward launch");
+}
+
 // ---------------------------------------------------------------- IPC
 namespace {
 struct IpcMap {
@@ -955,11 +1230,12 @@ rc_status rc_reserve_workspace(size_t bytes, rc_stream_t stream) {
 rc_status rc_stream_status(rc_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "stream");
-  unsigned int timeouts = 0, fold_timeouts = 0;
+  unsigned int timeouts = 0, fold_timeouts = 0, ce_timeouts = 0;
   e = read_and_clear_wait_timeouts(&timeouts);
   if (e == cudaSuccess) e = read_and_clear_fold_timeouts(&fold_timeouts);
+  if (e == cudaSuccess) e = read_and_clear_ce_timeouts(&ce_timeouts);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
-  timeouts += fold_timeouts;
+  timeouts += fold_timeouts + ce_timeouts;
   if (timeouts) return fail(RC_ERR_TIMEOUT, "%u bounded device wait(s) gave up", timeouts);
   return RC_OK;
 }

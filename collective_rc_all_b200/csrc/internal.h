@@ -120,6 +120,67 @@ struct A2aJob {
   int esz;
 };
 
+// Dropout over p rank buffers (dropout.cu), or behind the flat all-reduce.
+struct DropoutJob {
+  const void *x[kMaxP];
+  const void *res[kMaxP];  // residuals, all NULL when none is added
+  void *y[kMaxP];
+  int p;
+  uint64_t n;
+  int dt;
+  uint64_t seed, offset, rank_stride;
+  uint32_t thr;  // an element is dropped when its 16 random bits are below
+  float factor;  // of what is kept
+  bool reduce;   // y[r] = res[r] + drop(sum of x) instead of res[r] + drop(x[r])
+};
+
+// Mixture-of-experts gate over p ranks' tokens (gate.cu).
+struct GateJob {
+  const void *logits[kMaxP];
+  const uint8_t *mask[kMaxP];
+  int32_t *ids[kMaxP];
+  float *weights[kMaxP];
+  int32_t *counts[kMaxP];
+  const float *dweights[kMaxP];
+  void *dlogits[kMaxP];
+  float *stats, *loss;
+  const float *dloss;
+  void *ws;
+  int p, experts, top_k, dt;
+  uint64_t tokens;
+  bool normalize, backward;
+  float coef;
+};
+
+// Cross entropy over the ranks' vocabulary pieces (vocab_ce.cu).
+struct CeShape {
+  int64_t tokens, vocab;
+  int d, p;
+};
+struct CeJob {
+  CeShape shape;
+  const void *hidden;
+  const void *weight[kMaxP];
+  const int32_t *target;
+  int ignore;
+  float *loss, *lse;               // forward
+  const float *lse_in, *dloss;     // backward
+  void *dhidden, *dweight[kMaxP];  // backward
+  void *ws;
+  bool backward;
+};
+
+cudaError_t launch_dropout(const DropoutJob &job, cudaStream_t s);
+int gate_max_blocks(int p);
+size_t gate_workspace(int p, int experts);
+cudaError_t launch_gate(const GateJob &job, cudaStream_t s);
+// Workspace of a shape (`copies`: the operands must be copied to be aligned),
+// and of a job by its buffers' alignment.
+size_t ce_workspace(const CeShape &s, bool backward, bool copies);
+size_t ce_workspace(const CeJob &j);
+cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s);
+cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s);
+cudaError_t read_and_clear_ce_timeouts(unsigned int *count);
 cudaError_t launch_reduce(const ReduceJob &job, cudaStream_t s);
 bool fold_tma_eligible(const FoldJob &job);
 cudaError_t launch_fold_tma(const FoldJob &job, cudaStream_t s);

@@ -352,6 +352,128 @@ rc_status rc_zero1_step(const void *const *grads, void *const *params, float *co
                         const rc_adamw_hparams *hp, rc_stream_t stream);
 
 /*
+ * Dropout from a counter-based generator, over p rank buffers:
+ *   recv[r][i] = residual[r][i] + (kept ? factor * send[r][i] : 0)
+ * (without the residual when `residual` is NULL), in binary32 with one
+ * rounding per operation, cast to dt once.  The mask is a function of the
+ * element's index e = offset + r * rank_stride + i (modulo 2^64) and of
+ * `seed`, so it is never stored: the same call on a gradient, without the
+ * residual, is the backward pass.  Element e takes half word e % 8 (the low
+ * half of each 32-bit word first) of the Philox4x32-10 block with counter
+ * (e / 8, 0) and key seed (low word first); it is kept when that half word is
+ * at least t = rint(prob * 2^16).  factor = scale / (1 - t / 2^16), rounded
+ * to binary32 once, so the expectation is exact for the probability drawn.
+ *  - rank_stride 0 gives every rank the same mask (a replicated activation);
+ *    rank_stride n gives every rank its own (data-parallel ranks, or the
+ *    shards of one sequence).  Calls of a step take disjoint index ranges.
+ *  - prob in [0, 1].  A dropped element is zero whatever it held (NaN and
+ *    infinities too); t = 2^16 drops everything.
+ *  - dt RC_FP32 or RC_BF16.  In place (recv[r] == send[r] or residual[r]) is
+ *    allowed.  One launch, no workspace.
+ */
+rc_status rc_dropout(const void *const *send, const void *const *residual, void *const *recv, int p, size_t n,
+                     rc_dtype dt, float scale, double prob, uint64_t seed, uint64_t offset, uint64_t rank_stride,
+                     rc_stream_t stream);
+
+/*
+ * All-reduce (SUM) with dropout and the residual add behind it, in one pass:
+ * the end of a row-parallel layer, whose ranks hold partial sums and leave
+ * with the same activation.
+ *   recv[r][i] = cast(residual[r][i] + (kept ? factor * fold_r send[r][i] : 0))
+ * with rc_all_reduce's fold order, rc_dropout's mask for rank_stride 0, and
+ * one rounding to dt at the end (the fold's own is not rounded to bf16 in
+ * between).  The gradient of every send[r] is rc_dropout of rank r's incoming
+ * gradient with the same prob, seed, offset and scale, and rank_stride 0.
+ * In place is allowed as in rc_dropout.
+ */
+rc_status rc_all_reduce_dropout(const void *const *send, const void *const *residual, void *const *recv, int p,
+                                size_t n, rc_dtype dt, float scale, double prob, uint64_t seed, uint64_t offset,
+                                rc_stream_t stream);
+
+/*
+ * Mixture-of-experts gate over the tokens of p ranks [A2A]: the softmax of
+ * each token's router logits, its top_k experts, the counts that the dispatch
+ * (rc_all_to_all_v) needs, and the balance loss over all ranks' tokens.
+ *  logits[r]: [tokens][experts] of dt (RC_FP32 / RC_BF16), read.
+ *  token_mask[r]: [tokens] bytes, 0 = padding (token_mask NULL: none).
+ *  ids[r]: [tokens][top_k] chosen experts, largest logit first, ties to the
+ *    lowest index.  weights[r]: their probabilities, divided by their sum
+ *    when `normalize` is not 0.
+ *  counts[r]: [experts] choices of rank r's tokens.
+ *  stats: 2 * experts + 1 floats: f_e = choices of e / (top_k * M), P_e = the
+ *    mean probability of e, and M = the tokens that count, over all ranks.
+ *  loss: one float, coef * experts * sum_e f_e P_e (0 when M = 0).
+ * An expert whose logit is -inf or NaN is never chosen; a slot that finds no
+ * expert holds id -1 and weight 0.  A masked token, or one whose logits are
+ * all -inf, gets id -1 and weight 0 in every slot and counts nowhere.  A NaN
+ * or +inf logit makes its token's weights, P and the loss NaN.
+ * experts in [1, 512], top_k in [1, 16].  tokens 0 writes zero counts, stats
+ * and loss.  workspace: device memory of rc_moe_gate_workspace bytes, 16-byte
+ * aligned, the caller's for the time of the call (and of every replay of a
+ * graph that captured it).  Sums are binary32 in a fixed order.
+ */
+rc_status rc_moe_gate_workspace(int p, int experts, size_t *bytes);
+rc_status rc_moe_gate(const void *const *logits, const uint8_t *const *token_mask, int32_t *const *ids,
+                      float *const *weights, int32_t *const *counts, float *stats, float *loss, int p, size_t tokens,
+                      int experts, int top_k, rc_dtype dt, int normalize, float coef, void *workspace,
+                      size_t workspace_bytes, rc_stream_t stream);
+
+/*
+ * Gradient of rc_moe_gate to the logits, from the gradient of the chosen
+ * weights (dweights, [tokens][top_k] fp32 per rank; NULL: zero) and of the
+ * loss (dloss, one float; NULL: zero).  The counts carry no gradient.  ids
+ * and stats are rc_moe_gate's for the same logits, mask and options.  Masked
+ * tokens get zero.  dlogits[r] may be logits[r].
+ */
+rc_status rc_moe_gate_backward(const void *const *logits, const uint8_t *const *token_mask, const int32_t *const *ids,
+                               const float *const *dweights, const float *stats, const float *dloss,
+                               void *const *dlogits, int p, size_t tokens, int experts, int top_k, rc_dtype dt,
+                               int normalize, float coef, rc_stream_t stream);
+
+/*
+ * Softmax cross entropy over a vocabulary whose rows are cut into the ranks'
+ * pieces (a tensor-parallel output head), without keeping the logits.  Rank
+ * r's piece weight[r] holds rows [r*C, min((r+1)*C, vocab)), C = ceil(vocab/p)
+ * (the chunks of the collectives; a rank past the end holds none).
+ *   z_iv = sum_k hidden[i][k] W[v][k]          (bf16 products, fp32 sums)
+ *   lse_i = log sum_v exp z_iv,  loss_i = lse_i - z_{i, target_i}
+ *  hidden: [tokens][d] bf16.  weight[r]: [rows][d] bf16.  target: [tokens].
+ *  loss, lse: [tokens] fp32, written.
+ * target_i == ignore_index gives loss 0 (lse is computed); any other target
+ * outside [0, vocab) gives loss NaN.  dt must be RC_BF16 (RC_FP32:
+ * RC_ERR_UNSUPPORTED).  d in [1, 2^20].  tokens 0 returns RC_OK and launches
+ * nothing.
+ *
+ * workspace: device memory, 16-byte aligned, the caller's for the time of the
+ * call (and of every replay of a graph that captured it), of
+ * rc_vocab_ce_workspace bytes: room for the forward call, and when `backward`
+ * is not 0 for the backward call too.  `unaligned` not 0 makes room for copies
+ * of hidden and weight, which the calls need when one of them is not 16-byte
+ * aligned or d is not a multiple of 8 (the latter is taken into account by
+ * itself).  Nothing is kept in it from one call to the next.
+ */
+rc_status rc_vocab_ce_workspace(size_t tokens, size_t d, size_t vocab, int p, rc_dtype dt, int backward, int unaligned,
+                                size_t *bytes);
+rc_status rc_vocab_ce_forward(const void *hidden, const void *const *weight, const int32_t *target, float *loss,
+                              float *lse, size_t tokens, size_t d, size_t vocab, int p, rc_dtype dt,
+                              int32_t ignore_index, void *workspace, size_t workspace_bytes, rc_stream_t stream);
+
+/*
+ * Gradients of rc_vocab_ce_forward from the gradient dloss of each token's
+ * loss ([tokens] fp32) and its lse:
+ *   G_iv = dloss_i * (exp(z_iv - lse_i) - [v == target_i])   (0 if ignored)
+ *   dhidden = sum over the ranks of G_r W_r,   dweight[r] = G_r^T hidden
+ * dhidden [tokens][d] and dweight[r] [rows][d] bf16 are written, not added
+ * to.  What an ignored token's hidden row holds (NaN too) does not reach
+ * dweight; its dhidden row is zero.  A target outside [0, vocab) that is not
+ * ignore_index makes the gradients NaN.  tokens 0 sets dweight to zero.
+ */
+rc_status rc_vocab_ce_backward(const void *hidden, const void *const *weight, const int32_t *target, const float *lse,
+                               const float *dloss, void *dhidden, void *const *dweight, size_t tokens, size_t d,
+                               size_t vocab, int p, rc_dtype dt, int32_t ignore_index, void *workspace,
+                               size_t workspace_bytes, rc_stream_t stream);
+
+/*
  * Rank view [P2P]: one rank's share of a collective, for rank-per-GPU
  * execution -- one process per GPU, each reaching the other ranks' buffers
  * through peer mappings (rc_ipc_import).  The pointer arrays hold the p

@@ -1,0 +1,325 @@
+"""rc_moe_gate and rc_moe_gate_backward against the definition in 64 bits:
+sizes around the lanes' and blocks' borders, ties, masks that leave tokens,
+ranks or everything empty, -inf / NaN / infinite logits, gradients against the
+formula and against differences, refusals, capture."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -24  # half a step of binary32
+
+
+@pytest.fixture(scope="module")
+def rc():
+    import collective_rc_all_b200 as m
+    assert torch.cuda.is_available()
+    return m
+
+
+def guarded(*shape, dtype=torch.float32, shift=0):
+    """A tensor inside a buffer whose other elements hold 77."""
+    n = int(np.prod(shape))
+    buf = torch.full((shift + n + 64,), 77, dtype=dtype, device="cuda")
+    return buf[shift:shift + n].view(*shape), buf
+
+
+def untouched(pairs, shift=0):
+    for t, buf in pairs:
+        assert bool((buf[shift + t.numel():] == 77).all()) and bool((buf[:shift] == 77).all())
+
+
+class Gate:
+    """Outputs of one call, with guards behind every buffer."""
+
+    def __init__(self, rc, logits, k, mask=None, norm=True, coef=0.02, ws=None, stream=None):
+        p, (t, e) = len(logits), logits[0].shape
+        g = [[guarded(t, k, dtype=torch.int32) for _ in range(p)], [guarded(t, k) for _ in range(p)],
+             [guarded(e, dtype=torch.int32) for _ in range(p)], [guarded(2 * e + 1)], [guarded(1)]]
+        self.ids, self.weights, self.counts = ([x[0] for x in xs] for xs in g[:3])
+        self.stats, self.loss = g[3][0][0], g[4][0][0]
+        self.guards = [x for xs in g for x in xs]
+        self.call = lambda: rc.rc_moe_gate(logits, self.ids, self.weights, self.counts, self.stats, self.loss,
+                                           token_mask=mask, normalize=norm, coef=coef, workspace=ws, stream=stream)
+        self.call()
+
+
+def reference(logits, k, mask, norm, coef):
+    """ids, weights, counts, f, P, M, loss, probabilities, chosen in 64 bits; every row by itself."""
+    p, (t, e) = len(logits), logits[0].shape
+    z = torch.stack([x.double() for x in logits]).cpu().numpy()
+    ids, w, prob = np.full((p, t, k), -1), np.zeros((p, t, k)), np.zeros((p, t, e))
+    live = np.zeros((p, t), bool)
+    for r in range(p):
+        for i in range(t):
+            row = z[r, i]
+            if (mask is not None and not bool(mask[r][i])) or np.all(row == -np.inf):
+                continue
+            live[r, i] = True
+            ex = np.exp(row - row.max())
+            prob[r, i] = ex / ex.sum()
+            order = sorted((j for j in range(e) if row[j] > -np.inf), key=lambda j: (-row[j], j))[:k]
+            ids[r, i, :len(order)] = order
+            w[r, i, :len(order)] = prob[r, i, order] / (prob[r, i, order].sum() if norm else 1.0)
+    counts = np.stack([np.bincount(ids[r][ids[r] >= 0], minlength=e)[:e] for r in range(p)]) if t else np.zeros((p, e))
+    m = live.sum()
+    f, mean = counts.sum(0) / (k * max(m, 1)), prob.sum((0, 1)) / max(m, 1)
+    return dict(ids=ids, w=w, counts=counts, f=f, mean=mean, m=m, loss=coef * e * (f * mean).sum(), prob=prob, live=live)
+
+
+def spread(logits):
+    z = torch.stack([x.double() for x in logits])
+    z = z[torch.isfinite(z)]
+    return float(z.max() - z.min()) if z.numel() else 0.0
+
+
+def check_forward(g, ref, logits, e):
+    p, t = len(logits), logits[0].shape[0]
+    # binary32: the exponent's argument (|z - max| U), expf (4 U), the row sum (E U) and four more operations
+    rel = (spread(logits) + e + 16) * U
+    for r in range(p):
+        assert np.array_equal(g.ids[r].cpu().numpy(), ref["ids"][r])
+        assert np.array_equal(g.counts[r].cpu().numpy(), ref["counts"][r])
+        w = g.weights[r].double().cpu().numpy()
+        assert np.all(np.abs(w - ref["w"][r]) <= 2 * rel * np.abs(ref["w"][r]) + 1e-37)
+    s = g.stats.double().cpu().numpy()
+    more = rel + (p * t + 16) * U  # the sum over the tokens, in any order
+    assert s[2 * e] == ref["m"]
+    assert np.all(np.abs(s[:e] - ref["f"]) <= 4 * U * ref["f"])
+    assert np.all(np.abs(s[e:2 * e] - ref["mean"]) <= more * ref["mean"] + 1e-37)
+    assert abs(float(g.loss) - ref["loss"]) <= (more + (e + 8) * U) * abs(ref["loss"]) + 1e-37
+
+
+def make(p, t, e, dt, seed=0, scale=2.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return [(torch.randn(t, e, generator=gen, device="cuda") * scale).to(DT[dt]) for _ in range(p)]
+
+
+SHAPES = [(1, 1, 1, 1), (1, 1, 8, 2), (2, 3, 2, 2), (1, 65, 7, 3), (2, 129, 9, 1), (3, 40, 16, 16), (2, 100, 33, 4),
+          (8, 67, 64, 2), (1, 5, 60, 6), (2, 31, 128, 8), (4, 50, 130, 8), (1, 300, 256, 8), (2, 9, 257, 3), (1, 20, 512, 16)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("p,t,e,k", SHAPES)
+@pytest.mark.parametrize("norm", [False, True])
+def test_forward(rc, dt, p, t, e, k, norm):
+    z = make(p, t, e, dt, seed=t + e)
+    g = Gate(rc, z, k, norm=norm)
+    torch.cuda.synchronize()
+    check_forward(g, reference(z, k, None, norm, 0.02), z, e)
+    untouched(g.guards)
+
+
+def test_many_tokens_per_block(rc):
+    """More tokens than the grid takes in one step."""
+    z = make(1, 40000, 16, "bf16", seed=4)
+    g = Gate(rc, z, 2)
+    torch.cuda.synchronize()
+    x = z[0].double()
+    first = torch.sort(-x, dim=1, stable=True).indices[:, :2]
+    assert torch.equal(g.ids[0].long(), first)
+    assert torch.equal(g.counts[0].long(), torch.bincount(first.reshape(-1), minlength=16))
+    mean = torch.softmax(x, 1).mean(0)
+    assert float((g.stats[16:32].double() - mean).abs().max()) <= (40000 + 64) * U * float(mean.max())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_ties_go_to_the_lowest_index(rc, dt):
+    z = torch.zeros(6, 24, device="cuda")
+    z[1, 5:9] = 1.0
+    z[2, ::2] = -0.0                    # equal to +0
+    z[3] = -3.0
+    z[4, 23] = z[4, 0] = 7.0
+    z[5] = torch.arange(24, device="cuda") % 3
+    z = [z.to(DT[dt])]
+    g = Gate(rc, z, 5, norm=False)
+    torch.cuda.synchronize()
+    check_forward(g, reference(z, 5, None, False, 0.02), z, 24)
+
+
+@pytest.mark.parametrize("kind", ["some", "one_rank", "all"])
+def test_masked_tokens(rc, kind):
+    p, t, e, k = 3, 50, 20, 3
+    z = make(p, t, e, "f32", seed=6)
+    mask = [torch.ones(t, dtype=torch.uint8, device="cuda") for _ in range(p)]
+    for r in range(p):
+        if kind == "some":
+            mask[r][r::3] = 0
+        if kind == "all" or (kind == "one_rank" and r == 1):
+            mask[r][:] = 0
+        z[r][mask[r] == 0] = float("nan")  # whatever padding holds stays out
+    g = Gate(rc, z, k, mask=mask)
+    d = [torch.full_like(x, 9.0) for x in z]
+    rc.rc_moe_gate_backward(z, g.ids, g.stats, d, dweights=[torch.ones(t, k, device="cuda")] * p, dloss=torch.ones(1, device="cuda"),
+                            token_mask=mask, coef=0.02)
+    torch.cuda.synchronize()
+    clean = [torch.where(m[:, None] != 0, x, torch.zeros_like(x)) for x, m in zip(z, mask)]
+    check_forward(g, reference(clean, k, mask, True, 0.02), clean, e)
+    for r in range(p):
+        assert bool(torch.isfinite(d[r]).all()) and bool((d[r][mask[r] == 0] == 0).all())
+
+
+def test_minus_infinity_and_non_finite_logits(rc):
+    e, k = 12, 4
+    z = make(1, 8, e, "f32", seed=9)[0]
+    z[1] = -math.inf                     # an empty row
+    z[2, 2:] = -math.inf                 # fewer experts than slots
+    z[3, ::2] = -math.inf
+    z[4] = torch.finfo(torch.float32).min  # the type's lowest value is a number
+    g = Gate(rc, [z], k)
+    torch.cuda.synchronize()
+    check_forward(g, reference([z], k, None, True, 0.02), [z[[0, 1, 2, 3, 5, 6, 7]]], e)
+    bad = z.clone()
+    bad[6, 3] = math.nan
+    bad[7, 1] = math.inf
+    h = Gate(rc, [bad], k)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(h.loss).all()) and bool(torch.isnan(h.weights[0][6]).all())
+    assert torch.equal(h.ids[0][:6], g.ids[0][:6]) and torch.equal(h.weights[0][:6], g.weights[0][:6])
+    ids = h.ids[0].cpu()
+    assert 3 not in ids[6].tolist() and ids[7, 0] == 1 and bool(((ids >= -1) & (ids < e)).all())
+
+
+def test_no_tokens(rc):
+    z = [torch.empty(0, 10, device="cuda") for _ in range(2)]
+    g = Gate(rc, z, 2)
+    torch.cuda.synchronize()
+    assert int(g.counts[0].abs().sum()) == int(g.counts[1].abs().sum()) == 0
+    assert bool((g.stats == 0).all()) and float(g.loss) == 0.0
+    rc.rc_moe_gate_backward(z, g.ids, g.stats, z, dloss=g.loss, coef=0.02)
+
+
+def dlogits_reference(logits, ref, k, norm, coef, dw, dloss):
+    """Gradient and the size of its terms (for the tolerance), in 64 bits."""
+    p, (t, e) = len(logits), logits[0].shape
+    a = dloss * coef * e * ref["f"] / max(ref["m"], 1)
+    out, size = np.zeros((p, t, e)), np.zeros((p, t, e))
+    for r in range(p):
+        for i in range(t):
+            if not ref["live"][r, i]:
+                continue
+            pr = ref["prob"][r, i]
+            out[r, i] = pr * (a - pr @ a)
+            size[r, i] = pr * (np.abs(a) + pr @ np.abs(a))
+            for s in range(k):
+                j = ref["ids"][r, i, s]
+                if j < 0:
+                    continue
+                w, d = ref["w"][r, i], dw[r, i]
+                # d w_s / d z_j: a softmax over the chosen (normalised) or over all
+                out[r, i, j] += w[s] * d[s]
+                size[r, i, j] += w[s] * abs(d[s])
+                for u in range(e):
+                    share = sum(w[v] for v in range(k) if ref["ids"][r, i, v] == u) if norm else pr[u]
+                    out[r, i, u] -= w[s] * d[s] * share
+                    size[r, i, u] += w[s] * abs(d[s]) * share
+    return out, size
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("p,t,e,k", [(1, 1, 1, 1), (2, 17, 8, 2), (2, 9, 7, 3), (3, 12, 33, 4), (1, 11, 64, 8), (2, 5, 256, 8), (1, 3, 300, 5)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_backward(rc, dt, p, t, e, k, norm):
+    z = make(p, t, e, dt, seed=2 * t + e)
+    if e > 3:
+        z[0][0, 1:] = -math.inf            # one expert left, and an empty row
+        if t > 1:
+            z[0][1] = -math.inf
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dw = [torch.randn(t, k, generator=gen, device="cuda") for _ in range(p)]
+    dloss = torch.full((1,), 3.0, device="cuda")
+    mask = [(torch.rand(t, generator=gen, device="cuda") > 0.2).to(torch.uint8) for _ in range(p)]
+    g = Gate(rc, z, k, mask=mask, norm=norm, coef=0.5)
+    d = [guarded(t, e, dtype=DT[dt]) for _ in range(p)]
+    rc.rc_moe_gate_backward(z, g.ids, g.stats, [x[0] for x in d], dweights=dw, dloss=dloss, token_mask=mask, normalize=norm, coef=0.5)
+    torch.cuda.synchronize()
+    ref = reference(z, k, mask, norm, 0.5)
+    want, size = dlogits_reference(z, ref, k, norm, 0.5, torch.stack(dw).double().cpu().numpy(), 3.0)
+    # each term carries the forward's relative error a few times, and the result one rounding to its type
+    rel = 6 * (spread(z) + e + 24) * U
+    half = torch.finfo(DT[dt]).eps / 2
+    for r in range(p):
+        got = d[r][0].double().cpu().numpy()
+        assert np.all(np.abs(got - want[r]) <= rel * size[r] + half * (np.abs(want[r]) + rel * size[r]) + 1e-37)
+    untouched(d)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_backward_against_differences(rc, norm):
+    """The gradient of sum(dw * weights) + dloss * coef * E * sum f P with f held, by central differences in 64 bits."""
+    t, e, k, coef, h = 6, 10, 3, 0.3, 1e-5
+    z = make(1, t, e, "f32", seed=3)
+    dw = torch.randn(t, k, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    g = Gate(rc, z, k, norm=norm, coef=coef)
+    d = [torch.empty_like(z[0])]
+    rc.rc_moe_gate_backward(z, g.ids, g.stats, d, dweights=[dw], dloss=torch.ones(1, device="cuda"), normalize=norm, coef=coef)
+    ids, f = g.ids[0].long(), reference(z, k, None, norm, coef)["f"]
+    f = torch.from_numpy(f).cuda()
+
+    def value(x):
+        pr = torch.softmax(x, 1)
+        w = pr.gather(1, ids)
+        w = w / w.sum(1, keepdim=True) if norm else w
+        return (dw.double() * w).sum() + coef * e * (f * pr.mean(0)).sum()
+
+    x = z[0].double()
+    for i in range(t):
+        for j in range(0, e, 3):
+            step = torch.zeros_like(x)
+            step[i, j] = h
+            fd = float(value(x + step) - value(x - step)) / (2 * h)
+            assert abs(fd - float(d[0][i, j])) <= 1e-5 * (1 + abs(fd))   # h^2 third derivatives, and binary32
+
+
+def test_in_place_no_gradients_and_misaligned(rc):
+    p, t, e, k = 2, 37, 24, 2
+    z = make(p, t, e, "bf16", seed=8)
+    g = Gate(rc, z, k)
+    want = [torch.empty_like(x) for x in z]
+    dw = [torch.ones(t, k, device="cuda") for _ in range(p)]
+    one = torch.ones(1, device="cuda")
+    rc.rc_moe_gate_backward(z, g.ids, g.stats, want, dweights=dw, dloss=one)
+    zero = [torch.full_like(x, 5.0) for x in z]
+    rc.rc_moe_gate_backward(z, g.ids, g.stats, zero)
+    shifted = [guarded(t, e, dtype=torch.bfloat16, shift=1) for _ in range(p)]
+    for (s, _), x in zip(shifted, z):
+        s.copy_(x)
+    h = Gate(rc, [s for s, _ in shifted], k)
+    same = [x.clone() for x in z]
+    rc.rc_moe_gate_backward(same, g.ids, g.stats, same, dweights=dw, dloss=one)
+    rc.rc_moe_gate_backward([s for s, _ in shifted], h.ids, h.stats, [s for s, _ in shifted], dweights=dw, dloss=one)
+    torch.cuda.synchronize()
+    for r in range(p):
+        assert bool((zero[r] == 0).all())
+        assert torch.equal(same[r], want[r]) and torch.equal(shifted[r][0], want[r])
+        assert torch.equal(h.ids[r], g.ids[r]) and torch.equal(h.weights[r], g.weights[r])
+    untouched(shifted, shift=1)
+
+
+def test_two_graphs_with_their_own_workspaces_and_runs_repeat(rc):
+    z = [make(2, 500, 64, "bf16", seed=s) for s in (1, 2)]
+    want = [Gate(rc, x, 2) for x in z]
+    torch.cuda.synchronize()
+    graphs, outs, keep = [], [], []
+    for x in z:
+        ws = torch.empty(rc.rc_moe_gate_workspace(500, 64, 2), dtype=torch.uint8, device="cuda")
+        o = Gate(rc, x, 2, ws=ws)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            o.call()
+        graphs.append((g, torch.cuda.Stream()))
+        outs.append(o)
+        keep.append(ws)
+    for _ in range(5):
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a.stats, b.stats) and torch.equal(a.loss, b.loss)
+        assert all(torch.equal(x, y) for x, y in zip(a.ids + a.weights + a.counts, b.ids + b.weights + b.counts))

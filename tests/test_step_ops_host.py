@@ -1,0 +1,109 @@
+"""Argument checks of the dropout, gate and cross-entropy entry points on the
+host, before anything reaches a GPU.  CPU only."""
+import ctypes
+
+import pytest
+
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def rc():
+    import collective_rc_all_b200 as m
+    return m
+
+
+@pytest.fixture(autouse=True)
+def nothing_launched(rc):
+    n = rc.rc_launch_count()
+    yield
+    assert rc.rc_launch_count() == n
+
+
+def null(k):
+    return (ctypes.c_void_p * k)(*([0] * k))
+
+
+def test_dropout_arguments(rc):
+    L, a = rc.lib, null(16)
+    drop = lambda p=2, n=10, dt=0, prob=0.5, send=a: L.rc_dropout(send, None, a, p, n, dt, 1.0, prob, 1, 0, 0, None)  # noqa: E731
+    both = lambda p=2, n=10, dt=0, prob=0.5, send=a: L.rc_all_reduce_dropout(send, None, a, p, n, dt, 1.0, prob, 1, 0, None)  # noqa: E731
+    for call in (drop, both):
+        assert call(p=0) == 1 and call(p=17) == 1
+        assert call(dt=2) == 1 and call(dt=9) == 1
+        assert call(prob=-0.1) == 1 and call(prob=1.1) == 1 and call(prob=NAN) == 1
+        assert "prob" in rc.rc_last_error()
+        assert call(send=None) == 1
+        assert call() == 1 and "NULL" in rc.rc_last_error()
+        assert call(n=1 << 41) == 1
+        assert call(n=0) == 0
+
+
+def test_gate_arguments(rc):
+    L, a = rc.lib, null(16)
+    size = ctypes.c_size_t()
+
+    def fwd(p=2, t=8, e=16, k=2, dt=0, z=a, ws=None, nb=1 << 30):
+        return L.rc_moe_gate(z, None, a, a, a, None, None, p, t, e, k, dt, 1, 0.01, ws, nb, None)
+
+    def bwd(p=2, t=8, e=16, k=2, dt=0, z=a):
+        return L.rc_moe_gate_backward(z, None, a, None, None, None, a, p, t, e, k, dt, 1, 0.01, None)
+
+    for call in (fwd, bwd):
+        assert call(p=0) == 1 and call(p=17) == 1
+        assert call(dt=2) == 1
+        assert call(e=0) == 1 and call(e=513) == 1
+        assert call(k=0) == 1 and call(k=17, e=64) == 1 and call(k=5, e=4) == 1
+        assert call(t=1 << 31, k=2) == 1 and "32-bit" in rc.rc_last_error()
+        assert call(z=None) == 1
+        assert call() == 1 and "NULL" in rc.rc_last_error()
+    assert fwd(nb=16) == 1 and "too small" in rc.rc_last_error()
+    assert fwd(ws=8) == 1 and "aligned" in rc.rc_last_error()
+    assert bwd(t=0) == 0
+    assert L.rc_moe_gate_workspace(2, 16, None) == 1
+    assert L.rc_moe_gate_workspace(2, 513, ctypes.byref(size)) == 1
+    assert L.rc_moe_gate_workspace(2, 16, ctypes.byref(size)) == 0 and size.value > 0
+
+
+def test_cross_entropy_arguments(rc):
+    L, a = rc.lib, null(16)
+    size = ctypes.c_size_t()
+
+    def fwd(t=8, d=16, v=32, p=2, dt=1, w=a, ws=None, nb=1 << 40):
+        return L.rc_vocab_ce_forward(None, w, None, None, None, t, d, v, p, dt, -100, ws, nb, None)
+
+    def bwd(t=8, d=16, v=32, p=2, dt=1, w=a, ws=None, nb=1 << 40):
+        return L.rc_vocab_ce_backward(None, w, None, None, None, None, a, t, d, v, p, dt, -100, ws, nb, None)
+
+    def need(t=8, d=16, v=32, p=2, dt=1, **_):
+        return L.rc_vocab_ce_workspace(t, d, v, p, dt, 1, 0, ctypes.byref(size))
+
+    for call in (fwd, bwd, need):
+        assert call(p=0) == 1 and call(p=17) == 1
+        assert call(dt=0) == 2 and call(dt=2) == 1          # fp32 is a type of the library, not of this operator
+        assert call(d=0) == 1 and call(d=(1 << 20) + 1) == 1
+        assert call(v=0) == 1 and call(v=1 << 31) == 1 and call(t=1 << 31) == 1
+    for call in (fwd, bwd):
+        assert call(w=None) == 1
+        assert call(nb=16) == 1 and "too small" in rc.rc_last_error()
+        assert call(ws=8) == 1 and "aligned" in rc.rc_last_error()
+        assert call(ws=None) == 1 and "NULL" in rc.rc_last_error()
+    assert fwd(t=0) == 0
+    assert need(t=0) == 0 and size.value == 0
+    assert L.rc_vocab_ce_workspace(8, 16, 32, 2, 1, 1, 0, None) == 1
+
+
+def test_workspace_grows_with_what_is_asked(rc):
+    n = lambda **kw: rc.rc_vocab_ce_workspace(2048, 4096, 32000, 8, **kw)  # noqa: E731
+    assert n() < n(backward=True) < n(backward=True, unaligned=True)
+    # nothing of size tokens x vocab: far below the logits in 32 bits
+    assert rc.rc_vocab_ce_workspace(8192, 1024, 128000, 8, backward=True) < 8192 * 128000 * 4 // 8
+
+
+def test_lists_of_different_lengths_are_refused(rc):
+    with pytest.raises(ValueError):
+        rc.rc_dropout([1, 2], [1], 0.5, 1, n=4, dtype="f32", stream=0)
+    with pytest.raises(ValueError):
+        rc.rc_all_reduce_dropout([1, 2], [1, 2], 0.5, 1, residual=[1], n=4, dtype="f32", stream=0)
+    with pytest.raises(ValueError):
+        rc.rc_moe_gate([1, 2], [1], [1, 2], [1, 2], 1, 1, tokens=1, experts=2, top_k=1, dtype="f32", stream=0)

@@ -1,0 +1,322 @@
+"""rc_vocab_ce_forward / rc_vocab_ce_backward against the definition in 64
+bits: one token to thousands, widths and vocabularies that nothing divides,
+pieces shared unevenly, ignored and impossible targets, non-finite padding,
+misaligned buffers, differences, capture, streams.
+
+Tolerances.  A logit is a sum of d exact bf16 products kept in binary32 by the
+tensor cores, which may truncate: each 16-wide step is off by at most a few
+units of 2^-23 of the largest magnitude met, so |z error| <= Z = (d / 16 + 2) *
+2^-22 * max_v sum_k |h_k w_vk|.  lse and the target's logit carry Z once each,
+plus the exponentials and sums (2^-20 relative covers thousands of terms joined
+in trees, and the logarithm).  G carries (2 Z + 2^-20) of its size, the
+rounding to bf16 planes (half a step: 2^-8, or 2^-16 with two planes), its
+products the same kind of sum, and the results half a step of bf16."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+HALF = torch.finfo(torch.bfloat16).eps / 2  # 2^-8
+
+
+@pytest.fixture(scope="module")
+def rc():
+    import collective_rc_all_b200 as m
+    assert torch.cuda.is_available()
+    return m
+
+
+def rows_of(v, p):
+    c = -(-v // p)
+    return [max(0, min(v, (r + 1) * c) - r * c) for r in range(p)]
+
+
+def buffer(shape, dtype, shift=0):
+    n = int(np.prod(shape))
+    buf = torch.full((shift + n + 64,), 77, dtype=dtype, device="cuda")
+    return buf[shift:shift + n].view(*shape), buf
+
+
+class Case:
+    def __init__(self, tokens, d, vocab, p, seed=0, ignored=0.1, boost=6.0, shift=0, ignore=-100):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        self.tokens, self.d, self.vocab, self.p, self.ignore, self.shift = tokens, d, vocab, p, ignore, shift
+        w = (rnd(vocab, d) * d ** -0.5).bfloat16()
+        y = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
+        wy = w[y].float()
+        h = rnd(tokens, d) + wy / wy.square().sum(1, keepdim=True).clamp_min(1e-3) * boost * torch.rand(tokens, 1, generator=g, device="cuda")
+        skip = torch.rand(tokens, generator=g, device="cuda") < ignored
+        y[skip] = ignore
+        self.h, self.hb = buffer((tokens, d), torch.bfloat16, shift)
+        self.h.copy_(h)
+        self.w = []
+        for t in torch.split(w, rows_of(vocab, p)):
+            x, _ = buffer(tuple(t.shape), torch.bfloat16, shift)
+            x.copy_(t)
+            self.w.append(x)
+        self.y = y.int()
+        self.dloss = rnd(tokens) / max(tokens, 1)
+        f32 = lambda *s: buffer(s, torch.float32)  # noqa: E731
+        self.out = {"loss": f32(tokens), "lse": f32(tokens), "dh": buffer((tokens, d), torch.bfloat16, shift),
+                    **{f"dw{r}": buffer(tuple(t.shape), torch.bfloat16, shift) for r, t in enumerate(self.w)}}
+        for k, (t, _) in self.out.items():
+            setattr(self, k, t)
+        self.dw = [self.out[f"dw{r}"][0] for r in range(p)]
+
+    def forward(self, rc, **kw):
+        rc.rc_vocab_ce_forward(self.h, self.w, self.y, self.loss, self.lse, ignore_index=self.ignore, **kw)
+
+    def backward(self, rc, **kw):
+        rc.rc_vocab_ce_backward(self.h, self.w, self.y, self.lse, self.dloss, self.dh, self.dw, ignore_index=self.ignore, **kw)
+
+    def untouched(self):
+        for k, (t, buf) in self.out.items():
+            s = self.shift if k.startswith("d") else 0
+            assert bool((buf[s + t.numel():] == 77).all()) and bool((buf[:s] == 77).all()), k
+
+    def check(self, planes=None):
+        """Every output against 64 bits, element by element."""
+        planes = planes or (2 if self.tokens <= 128 else 1)
+        h, w = self.h.double(), torch.cat([x.double() for x in self.w])
+        live = self.y != self.ignore
+        h = torch.where(live[:, None], h, 0.0)
+        z = h @ w.T
+        size = (h.abs() @ w.abs().T).amax(1)
+        zerr = (self.d / 16 + 2) * 2.0 ** -22 * size
+        lse = torch.logsumexp(z, 1)
+        at = torch.where(live, self.y.long(), 0)
+        zt = z.gather(1, at[:, None])[:, 0]
+        small = 2.0 ** -20
+        tol = zerr + small * (1 + lse.abs())
+        assert bool(((self.lse.double() - lse).abs() <= tol)[live].all()), "lse"
+        loss = torch.where(live, lse - zt, 0.0)
+        tol = torch.where(live, 2 * zerr + small * (1 + lse.abs() + zt.abs()), 0.0)
+        assert bool(((self.loss.double() - loss).abs() <= tol).all()), "loss"
+        pr = torch.exp(z - lse[:, None])
+        one = torch.zeros_like(pr)
+        one[torch.arange(self.tokens, device="cuda")[live], at[live]] = 1.0
+        g = torch.where(live, self.dloss.double(), 0.0)[:, None]
+        G = g * (pr - one)
+        slack = g.abs() * pr * (2 * zerr[:, None] + 2 * small) + G.abs() * (HALF if planes == 1 else 2.0 ** -16)
+        # the target's own difference p - 1 is rounded to binary32
+        slack += g.abs() * one * 2.0 ** -23
+        steps = lambda k: (planes * k / 16 + 2) * 2.0 ** -22  # noqa: E731
+        dh = G @ w
+        tol = slack @ w.abs() + steps(self.vocab + 256 * self.p) * (G.abs() @ w.abs())
+        tol = tol + HALF * (dh.abs() + tol) + 1e-37
+        assert bool(((self.dh.double() - dh).abs() <= tol).all()), "dhidden"
+        dw = G.T @ h
+        tol = slack.T @ h.abs() + steps(self.tokens + 64) * (G.abs().T @ h.abs())
+        tol = tol + HALF * (dw.abs() + tol) + 1e-37
+        got = torch.cat([x.double() for x in self.dw])
+        assert bool(((got - dw).abs() <= tol).all()), "dweight"
+        # as a whole: the two roundings to bf16, independent from entry to entry, stay below 2^-8 together
+        for a, b, what in ((self.dh.double(), dh, "dhidden"), (got, dw, "dweight")):
+            if float(b.norm()) > 0 and self.tokens >= 16:
+                assert float((a - b).norm()) <= 2.0 ** -8 * float(b.norm()), what
+
+
+SHAPES = [(1, 8, 2, 1), (1, 64, 1000, 4), (3, 16, 3, 8), (5, 64, 1000, 2), (7, 1, 40, 2), (128, 72, 257, 1), (129, 40, 300, 3),
+          (64, 512, 5000, 16), (257, 264, 700, 5), (300, 130, 1023, 3), (33, 1001, 511, 2), (200, 2056, 4100, 2), (513, 320, 2049, 8)]
+
+
+@pytest.mark.parametrize("tokens,d,vocab,p", SHAPES)
+def test_against_64_bits(rc, tokens, d, vocab, p):
+    c = Case(tokens, d, vocab, p, seed=tokens + d)
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+    c.untouched()
+
+
+def test_vocabulary_in_several_pieces(rc):
+    """G exceeds one piece of the workspace: dhidden adds over the pieces, the last one shorter."""
+    c = Case(3000, 128, 20011, 4, seed=1)
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+    c.untouched()
+
+
+@pytest.mark.parametrize("tokens,d", [(40, 64), (300, 65)])
+def test_misaligned_buffers(rc, tokens, d):
+    c = Case(tokens, d, 777, 3, seed=2, shift=1)
+    assert c.h.data_ptr() % 16 == 2
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+    c.untouched()
+
+
+@pytest.mark.parametrize("tokens", [20, 200])
+def test_every_token_ignored(rc, tokens):
+    c = Case(tokens, 64, 300, 2, ignored=2.0)
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    assert bool((c.loss == 0).all()) and bool((c.dh == 0).all()) and all(bool((x == 0).all()) for x in c.dw)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_padding_may_hold_anything(rc, bad):
+    """Rows of ignored tokens reach no output but their own lse."""
+    a, b = Case(150, 96, 600, 2, seed=3, ignored=0.3), Case(150, 96, 600, 2, seed=3, ignored=0.3)
+    skip = b.y == b.ignore
+    assert bool(skip.any())
+    b.h[skip] = bad
+    b.dloss[skip] = bad
+    for c in (a, b):
+        c.forward(rc)
+        c.backward(rc)
+    rc.rc_stream_status()
+    assert torch.equal(a.loss, b.loss) and torch.equal(a.lse[~skip], b.lse[~skip])
+    assert torch.equal(a.dh, b.dh) and all(torch.equal(x, y) for x, y in zip(a.dw, b.dw))
+
+
+def test_ignore_index_inside_the_vocabulary(rc):
+    c = Case(140, 48, 333, 2, seed=4, ignored=0.2, ignore=5)
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+
+
+@pytest.mark.parametrize("label", [-1, 333, 2**31 - 1, -2**31])
+def test_a_label_that_is_no_word_is_loud(rc, label):
+    a = Case(10, 48, 333, 2, seed=4, ignored=0.0)
+    a.y[3] = label
+    a.forward(rc)
+    a.backward(rc)
+    rc.rc_stream_status()
+    assert bool(torch.isnan(a.loss[3])) and int(torch.isnan(a.loss).sum()) == 1
+    assert bool(torch.isnan(a.dh[3]).all()) and bool(torch.isfinite(a.dh[:3]).all()) and bool(torch.isfinite(a.dh[4:]).all())
+    assert all(bool(torch.isnan(x).all()) for x in a.dw)
+
+
+def test_confident_and_far_logits(rc):
+    """Rows whose target has nearly all the probability, and logits of +-200."""
+    c = Case(64, 256, 900, 2, seed=5, boost=40.0)
+    c.h[::2] *= 50
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+
+
+def test_no_tokens(rc):
+    c = Case(0, 32, 100, 2)
+    for x in c.dw:
+        x.fill_(3.0)
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    assert all(bool((x == 0).all()) for x in c.dw)
+
+
+def test_gradients_against_differences(rc):
+    """Directional derivatives of sum(dloss * loss) in 64 bits along random
+    directions.  The gradients are bf16: half a step of every entry, and the
+    rounding of G, bound the sum."""
+    c = Case(40, 64, 500, 2, seed=6)
+    c.forward(rc)
+    c.backward(rc)
+    h, w = c.h.double(), torch.cat([x.double() for x in c.w])
+    live = c.y != c.ignore
+    at = torch.where(live, c.y.long(), 0)
+
+    def value(h, w):
+        z = h @ w.T
+        return (torch.where(live, c.dloss.double(), 0.0) * (torch.logsumexp(z, 1) - z.gather(1, at[:, None])[:, 0])).sum()
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dw = torch.cat([x.double() for x in c.dw])
+    for _ in range(4):
+        u = torch.randn(h.shape, generator=g, device="cuda", dtype=torch.float64)
+        v = torch.randn(w.shape, generator=g, device="cuda", dtype=torch.float64)
+        e = 1e-5
+        fd = float(value(h + e * u, w + e * v) - value(h - e * u, w - e * v)) / (2 * e)
+        got = float((c.dh.double() * u).sum() + (dw * v).sum())
+        room = float((c.dh.double() * u).abs().sum() + (dw * v).abs().sum())
+        assert abs(fd - got) <= 2 * HALF * room + 1e-7
+
+
+def test_runs_repeat_bit_for_bit(rc):
+    a, b = Case(700, 192, 3001, 4, seed=7), Case(700, 192, 3001, 4, seed=7)
+    for c in (a, b):
+        c.forward(rc)
+        c.backward(rc)
+    rc.rc_stream_status()
+    for k in a.out:
+        assert torch.equal(a.out[k][0], b.out[k][0]), k
+
+
+def test_the_pieces_do_not_change_the_loss_beyond_rounding(rc):
+    """One rank and eight ranks are the same operator."""
+    a, b = Case(90, 128, 1024, 1, seed=8), Case(90, 128, 1024, 8, seed=8)
+    for c in (a, b):
+        c.forward(rc)
+        c.backward(rc)
+    rc.rc_stream_status()
+    assert float((a.loss - b.loss).abs().max()) <= 1e-5
+    b.check()
+
+
+def test_two_graphs_replayed_at_once_and_other_streams(rc):
+    cases = [Case(300, 128, 2000, 2, seed=s) for s in (10, 11)]
+    want = []
+    for c in cases:
+        c.forward(rc)
+        c.backward(rc)
+        torch.cuda.synchronize()
+        want.append({k: t.clone() for k, (t, _) in c.out.items()})
+        for t, _ in c.out.values():
+            t.zero_()
+    graphs = []
+    for c in cases:
+        ws = torch.empty(rc.rc_vocab_ce_workspace(300, 128, 2000, 2, backward=True), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.forward(rc, workspace=ws)
+            c.backward(rc, workspace=ws)
+        graphs.append((g, torch.cuda.Stream(), ws))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, s, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        for k, (t, _) in c.out.items():
+            assert torch.equal(t, w[k]), k
+            t.zero_()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    cases[0].forward(rc, stream=side)          # workspace from torch, work on a stream that is not the current one
+    cases[0].backward(rc, stream=side)
+    side.synchronize()
+    for k, (t, _) in cases[0].out.items():
+        assert torch.equal(t, want[0][k]), k
+
+
+def test_refusals_launch_nothing(rc):
+    c = Case(20, 64, 300, 2)
+    n = rc.rc_launch_count()
+    ws = torch.empty(64, dtype=torch.uint8, device="cuda")
+    with pytest.raises(rc.RankCollError, match="too small"):
+        c.forward(rc, workspace=ws)
+    with pytest.raises(rc.RankCollError, match="unsupported"):
+        f = [x.float() for x in c.w]
+        rc.rc_vocab_ce_forward(c.h.float(), f, c.y, c.loss, c.lse, workspace=ws)
+    with pytest.raises(TypeError):
+        rc.rc_vocab_ce_forward(c.h, c.w, c.y.long(), c.loss, c.lse, workspace=ws)
+    with pytest.raises(ValueError):
+        rc.rc_vocab_ce_forward(c.h, [c.w[0][:-1], c.w[1]], c.y, c.loss, c.lse, workspace=ws)
+    with pytest.raises(rc.RankCollError, match="overlap"):
+        rc.rc_vocab_ce_backward(c.h, c.w, c.y, c.lse, c.dloss, c.h, c.dw)
+    assert rc.rc_launch_count() == n
