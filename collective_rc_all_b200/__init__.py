@@ -15,6 +15,7 @@ carrying the library's message.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence, Union
 
@@ -146,6 +147,18 @@ _DT_NAMES = {"f32": FP32, "fp32": FP32, "float32": FP32, "bf16": BF16, "bfloat16
 _OP_NAMES = {"sum": SUM, "max": MAX, "min": MIN}
 
 
+_torch = None
+
+
+def _torch_mod():
+    """torch, imported with the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _is_tensor(x) -> bool:
     return hasattr(x, "data_ptr") and hasattr(x, "dtype")
 
@@ -154,7 +167,7 @@ def _dt(dtype, like=None) -> int:
     if dtype is None:
         if like is None or not _is_tensor(like):
             raise ValueError("dtype is required when buffers are raw addresses")
-        import torch
+        torch = _torch_mod()
         m = {torch.float32: FP32, torch.bfloat16: BF16, torch.int32: INT32}
         if like.dtype not in m:
             raise TypeError(f"unsupported tensor dtype {like.dtype}")
@@ -163,7 +176,7 @@ def _dt(dtype, like=None) -> int:
         return _DT_NAMES[dtype.lower()]
     if isinstance(dtype, int):
         return dtype
-    import torch
+    torch = _torch_mod()
     return {torch.float32: FP32, torch.bfloat16: BF16, torch.int32: INT32}[dtype]
 
 
@@ -172,7 +185,7 @@ def _op(op) -> int:
 
 
 def _addr(x) -> int:
-    if _is_tensor(x):
+    if type(x) is not int and _is_tensor(x):
         if not x.is_cuda:
             raise ValueError("tensor is not on a CUDA device")
         if not x.is_contiguous():
@@ -187,8 +200,8 @@ def _ptrs(xs: Sequence) -> "ctypes.Array":
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch_mod()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
@@ -445,18 +458,44 @@ def _same_len(p: int, **lists) -> None:
             raise ValueError(f"{name} holds {len(xs)} buffers for {p} ranks")
 
 
-def _want(x, dtype: str, shape, what: str) -> None:
-    """A tensor's element type and shape (raw addresses are the caller's)."""
-    if x is None or not _is_tensor(x):
-        return
-    if str(x.dtype) not in ("torch." + dtype, "torch.bool" if dtype == "uint8" else ""):
-        raise TypeError(f"{what} must be {dtype}, not {x.dtype}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+def _typed(x, dtype, shape, what: str) -> Optional[int]:
+    """Address of a buffer; a tensor's element type and shape are checked (a
+    raw address is the caller's word), None stays None.  That it is memory of
+    the current device is the library's check."""
+    if x is None or type(x) is int:
+        return x
+    if not isinstance(x, _torch_mod().Tensor):
+        return int(x)
+    if x.dtype not in dtype:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtype)}, not {x.dtype}")
+    if shape is not None and x.shape != shape:
         raise ValueError(f"{what} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return x.data_ptr()
 
 
-def _float_name(dt: int) -> str:
-    return {FP32: "float32", BF16: "bfloat16"}.get(dt, "float32")
+def _typed_ptrs(xs, dtype, shapes, what: str):
+    """A pointer array of _typed addresses; shapes: one for all, or a list of
+    one for each.  Buffers like the first one pass on their element count."""
+    if xs is None:
+        return None
+    if isinstance(shapes, list):
+        return (ctypes.c_void_p * len(xs))(*[_typed(x, dtype, s, what) for x, s in zip(xs, shapes)])
+    out = [_typed(xs[0], dtype, shapes, what)]
+    tensor, first, n, dims = _torch_mod().Tensor, dtype[0] if dtype else None, math.prod(shapes), len(shapes)
+    for x in xs[1:]:
+        if type(x) is tensor and x.dtype is first and x.numel() == n and x.dim() == dims and x.is_contiguous():
+            out.append(x.data_ptr())
+        else:
+            out.append(_typed(x, dtype, shapes, what))
+    return (ctypes.c_void_p * len(out))(*out)
+
+
+def _types():
+    """(float32, int32, byte masks) as sets of torch types, and the library's floating types by code."""
+    t = _torch_mod()
+    return (t.float32,), (t.int32,), (t.uint8, t.bool), {FP32: (t.float32,), BF16: (t.bfloat16,)}
 
 
 def _workspace(ws, nbytes: int, stream):
@@ -466,7 +505,7 @@ def _workspace(ws, nbytes: int, stream):
         if not _is_tensor(ws):
             raise TypeError("workspace must be a CUDA tensor")
         return _addr(ws), ws.numel() * ws.element_size(), ws
-    import torch
+    torch = _torch_mod()
     ws = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device="cuda")
     s = _stream(stream)
     if s != torch.cuda.current_stream().cuda_stream:
@@ -523,25 +562,20 @@ def rc_moe_gate(logits: Sequence[Buf], ids: Sequence[Buf], weights: Sequence[Buf
     """Top-k experts of every token, their weights, per-rank counts, and the
     balance loss over all ranks.  logits[r] is [tokens, experts], ids[r]
     (int32) and weights[r] (float32) [tokens, top_k], counts[r] (int32)
-    [experts], stats 2 * experts + 1 floats, loss one float."""
+    [experts], token_mask[r] (uint8 or bool) [tokens], stats 2 * experts + 1
+    floats, loss one float."""
     p = len(logits)
     _same_len(p, ids=ids, weights=weights, counts=counts, token_mask=token_mask)
     t, e, k = _gate_sizes(logits, ids, tokens, experts, top_k)
     dt = _dt(dtype, logits[0])
-    for r in range(p):
-        _want(logits[r], _float_name(dt), (t, e), f"logits[{r}]")
-        _want(ids[r], "int32", (t, k), f"ids[{r}]")
-        _want(weights[r], "float32", (t, k), f"weights[{r}]")
-        _want(counts[r], "int32", (e,), f"counts[{r}]")
-        if token_mask is not None:
-            _want(token_mask[r], "uint8", (t,), f"token_mask[{r}]")
-    _want(stats, "float32", (2 * e + 1,), "stats")
-    _want(loss, "float32", None, "loss")
+    f32, i32, byte, kinds = _types()
     need = 0 if workspace is not None else rc_moe_gate_workspace(t, e, p)
     ws, nbytes, _keep = _workspace(workspace, need, stream)
-    _check(lib.rc_moe_gate(_ptrs(logits), _opt_ptrs(token_mask), _ptrs(ids), _ptrs(weights), _ptrs(counts),
-                           _addr(stats), _addr(loss), p, t, e, k, dt, int(bool(normalize)), coef, ws, nbytes,
-                           _stream(stream)), "rc_moe_gate")
+    _check(lib.rc_moe_gate(_typed_ptrs(logits, kinds.get(dt, ()), (t, e), "logits"),
+                           _typed_ptrs(token_mask, byte, (t,), "token_mask"), _typed_ptrs(ids, i32, (t, k), "ids"),
+                           _typed_ptrs(weights, f32, (t, k), "weights"), _typed_ptrs(counts, i32, (e,), "counts"),
+                           _typed(stats, f32, (2 * e + 1,), "stats"), _typed(loss, f32, None, "loss"), p, t, e, k, dt,
+                           int(bool(normalize)), coef, ws, nbytes, _stream(stream)), "rc_moe_gate")
 
 
 def rc_moe_gate_backward(logits: Sequence[Buf], ids: Sequence[Buf], stats: Buf, dlogits: Sequence[Buf],
@@ -554,18 +588,13 @@ def rc_moe_gate_backward(logits: Sequence[Buf], ids: Sequence[Buf], stats: Buf, 
     _same_len(p, ids=ids, dlogits=dlogits, dweights=dweights, token_mask=token_mask)
     t, e, k = _gate_sizes(logits, ids, tokens, experts, top_k)
     dt = _dt(dtype, logits[0])
-    for r in range(p):
-        _want(logits[r], _float_name(dt), (t, e), f"logits[{r}]")
-        _want(dlogits[r], _float_name(dt), (t, e), f"dlogits[{r}]")
-        _want(ids[r], "int32", (t, k), f"ids[{r}]")
-        if dweights is not None:
-            _want(dweights[r], "float32", (t, k), f"dweights[{r}]")
-        if token_mask is not None:
-            _want(token_mask[r], "uint8", (t,), f"token_mask[{r}]")
-    _want(stats, "float32", (2 * e + 1,), "stats")
-    _want(dloss, "float32", None, "dloss")
-    _check(lib.rc_moe_gate_backward(_ptrs(logits), _opt_ptrs(token_mask), _ptrs(ids), _opt_ptrs(dweights), _addr(stats),
-                                    None if dloss is None else _addr(dloss), _ptrs(dlogits), p, t, e, k, dt,
+    f32, i32, byte, kinds = _types()
+    _check(lib.rc_moe_gate_backward(_typed_ptrs(logits, kinds.get(dt, ()), (t, e), "logits"),
+                                    _typed_ptrs(token_mask, byte, (t,), "token_mask"),
+                                    _typed_ptrs(ids, i32, (t, k), "ids"),
+                                    _typed_ptrs(dweights, f32, (t, k), "dweights"),
+                                    _typed(stats, f32, (2 * e + 1,), "stats"), _typed(dloss, f32, None, "dloss"),
+                                    _typed_ptrs(dlogits, kinds.get(dt, ()), (t, e), "dlogits"), p, t, e, k, dt,
                                     int(bool(normalize)), coef, _stream(stream)), "rc_moe_gate_backward")
 
 
@@ -590,11 +619,8 @@ def _ce_sizes(hidden, weight, tokens, d, vocab, dtype):
         vocab = sum(w.shape[0] for w in weight)
     p, dt = len(weight), _dt(dtype, hidden)
     c = -(-int(vocab) // p)
-    rows = [max(0, min(int(vocab), (r + 1) * c) - r * c) for r in range(p)]
-    _want(hidden, _float_name(dt), (tokens, d), "hidden")
-    for r, w in enumerate(weight):
-        _want(w, _float_name(dt), (rows[r], d), f"weight[{r}]")
-    return int(tokens), int(d), int(vocab), p, dt, rows
+    shapes = [(max(0, min(int(vocab), (r + 1) * c) - r * c), int(d)) for r in range(p)]
+    return int(tokens), int(d), int(vocab), p, dt, shapes
 
 
 def _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, backward, stream):
@@ -610,31 +636,30 @@ def rc_vocab_ce_forward(hidden: Buf, weight: Sequence[Buf], target: Buf, loss: B
     """Cross entropy of every token over the ranks' vocabulary pieces:
     hidden [tokens, d], weight[r] [rows, d] (bf16), target (int32) [tokens];
     loss and lse (float32) [tokens] are written."""
-    t, d, v, p, dt, _ = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
-    _want(target, "int32", (t,), "target")
-    _want(loss, "float32", (t,), "loss")
-    _want(lse, "float32", (t,), "lse")
+    t, d, v, p, dt, shapes = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
+    f32, i32, _, kinds = _types()
+    kind = kinds.get(dt, ())
     ws, nbytes, _keep = _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, False, stream)
-    _check(lib.rc_vocab_ce_forward(_addr(hidden), _ptrs(weight), _addr(target), _addr(loss), _addr(lse), t, d, v, p, dt,
-                                   int(ignore_index), ws, nbytes, _stream(stream)), "rc_vocab_ce_forward")
+    _check(lib.rc_vocab_ce_forward(_typed(hidden, kind, (t, d), "hidden"), _typed_ptrs(weight, kind, shapes, "weight"),
+                                   _typed(target, i32, (t,), "target"), _typed(loss, f32, (t,), "loss"),
+                                   _typed(lse, f32, (t,), "lse"), t, d, v, p, dt, int(ignore_index), ws, nbytes,
+                                   _stream(stream)), "rc_vocab_ce_forward")
 
 
 def rc_vocab_ce_backward(hidden: Buf, weight: Sequence[Buf], target: Buf, lse: Buf, dloss: Buf, dhidden: Buf,
                          dweight: Sequence[Buf], ignore_index: int = -100, workspace=None, tokens=None, d=None,
                          vocab=None, dtype=None, stream=None):
     """dhidden and dweight[r] from dloss (float32, [tokens]) and the forward's lse."""
-    t, d, v, p, dt, rows = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
+    t, d, v, p, dt, shapes = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
     _same_len(p, dweight=dweight)
-    _want(target, "int32", (t,), "target")
-    _want(lse, "float32", (t,), "lse")
-    _want(dloss, "float32", (t,), "dloss")
-    _want(dhidden, _float_name(dt), (t, d), "dhidden")
-    for r, w in enumerate(dweight):
-        _want(w, _float_name(dt), (rows[r], d), f"dweight[{r}]")
+    f32, i32, _, kinds = _types()
+    kind = kinds.get(dt, ())
     ws, nbytes, _keep = _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, True, stream)
-    _check(lib.rc_vocab_ce_backward(_addr(hidden), _ptrs(weight), _addr(target), _addr(lse), _addr(dloss),
-                                    _addr(dhidden), _ptrs(dweight), t, d, v, p, dt, int(ignore_index), ws, nbytes,
-                                    _stream(stream)), "rc_vocab_ce_backward")
+    _check(lib.rc_vocab_ce_backward(_typed(hidden, kind, (t, d), "hidden"), _typed_ptrs(weight, kind, shapes, "weight"),
+                                    _typed(target, i32, (t,), "target"), _typed(lse, f32, (t,), "lse"),
+                                    _typed(dloss, f32, (t,), "dloss"), _typed(dhidden, kind, (t, d), "dhidden"),
+                                    _typed_ptrs(dweight, kind, shapes, "dweight"), t, d, v, p, dt, int(ignore_index),
+                                    ws, nbytes, _stream(stream)), "rc_vocab_ce_backward")
 
 
 def rc_copy(src: Buf, dst: Buf, nbytes=None, stream=None):

@@ -96,8 +96,22 @@ MemGetAddressRangeFn address_range_fn() {
 // inside one allocation.
 // peer_ok: the memory may also belong to another device that the current
 // device can access (a peer mapping).
-rc_status check_device_range(const void *ptr, size_t bytes, const char *what, int idx, bool peer_ok = false) {
+// `seen`: allocations that this call has found to be the current device's; a
+// buffer inside one of them needs no further query (buffers from a caching
+// allocator often share an allocation, and a query of the driver costs more
+// than the rest of a buffer's checks).
+struct SeenRange {
+  uintptr_t lo, hi;
+};
+
+rc_status check_device_range(const void *ptr, size_t bytes, const char *what, int idx, bool peer_ok = false,
+                             std::vector<SeenRange> *seen = nullptr) {
   if (ptr == nullptr) return fail(RC_ERR_INVALID_ARG, "%s[%d] is NULL", what, idx);
+  if (seen) {
+    const uintptr_t p = (uintptr_t)ptr;
+    for (const SeenRange &r : *seen)
+      if (p >= r.lo && p < r.hi && bytes <= r.hi - p) return RC_OK;
+  }
   cudaPointerAttributes at{};
   cudaError_t e = cudaPointerGetAttributes(&at, ptr);
   if (e != cudaSuccess) {
@@ -128,6 +142,7 @@ rc_status check_device_range(const void *ptr, size_t bytes, const char *what, in
         return fail(RC_ERR_INVALID_ARG,
                     "%s[%d]=%p: %zu bytes run past the end of its allocation (%zu bytes at %p)", what,
                     idx, ptr, bytes, size, (void *)base);
+      if (seen) seen->push_back({(uintptr_t)base, (uintptr_t)base + size});
     }
   }
   return RC_OK;
@@ -178,11 +193,12 @@ rc_status check_aliasing(const std::vector<Buf> &bs) {
 }
 
 rc_status check_ranges(const std::vector<Buf> &bs, bool peer_ok = false) {
+  std::vector<SeenRange> seen;
   for (const Buf &b : bs) {
     if (b.esz > 1 && b.lo % (uintptr_t)b.esz != 0)
       return fail(RC_ERR_INVALID_ARG, "%s[%d]=%p is not aligned to its %d-byte elements", b.what, b.idx,
                   (void *)b.lo, b.esz);
-    rc_status st = check_device_range((const void *)b.lo, b.hi - b.lo, b.what, b.idx, peer_ok);
+    rc_status st = check_device_range((const void *)b.lo, b.hi - b.lo, b.what, b.idx, peer_ok, &seen);
     if (st != RC_OK) return st;
   }
   return RC_OK;

@@ -14,13 +14,19 @@
 //
 // A token's row lies in the registers of LPT lanes, VPL values each (a lane
 // owns VPL neighbouring experts), so a warp works on 32 / LPT tokens at once
-// and every reduction over a row is log2(LPT) shuffles.  The sums over tokens
-// (P_e, counts) stay in registers while a block walks its tokens and leave it
-// as one partial per block; a second launch adds the partials in block order,
-// so the results are the same on every run (no floating-point atomics).
+// and every reduction over a row is log2(LPT) shuffles (one redux for whole
+// warps).  The top k come from rounds over the lanes' best values; a lane
+// keeps its two best at hand and looks through its row again only when it
+// wins a third time.  The sums over tokens (P_e, counts) stay in registers
+// while a block walks its tokens and leave it as one partial per block; a
+// second launch (one cluster of 8 blocks, each an eighth of the experts) adds
+// the partials in block order, so the results are the same on every run (no
+// floating-point atomics).  Few tokens are one block's work altogether, in
+// one launch.
 #include <algorithm>
 #include <cmath>
 
+#include "bulk.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -28,8 +34,12 @@
 namespace rc {
 namespace {
 
-constexpr int kNT = 256;
+constexpr int kNT = 512;
 constexpr int kWarps = kNT / 32;
+constexpr int kBackNT = 256;
+constexpr int kMaxK = 16;
+constexpr int kStatBlocks = 8;  // the cluster of rc_gate_stats_kernel
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct GateParams {
   const char *z[kMaxRanks];
@@ -39,8 +49,7 @@ struct GateParams {
   int32_t *counts[kMaxRanks];
   const float *dw[kMaxRanks];  // backward; NULL: zero
   char *dz[kMaxRanks];
-  float *part_p;      // [p * blocks][E]
-  int32_t *part_c;    // [p * blocks][E]
+  float2 *part;       // [p * blocks][E]: sum of probabilities, choices (as bits)
   int32_t *part_m;    // [p * blocks]
   float *stats;       // f[E], P[E], M
   float *loss;
@@ -75,6 +84,19 @@ __device__ __forceinline__ void load_row(const char *row, int e0, int E, bool ve
   }
 }
 
+// The same for token t of a rank; nothing but -inf when there is no such token
+// or it is masked.
+template <class T, int VPL>
+__device__ __forceinline__ void load_token(const GateParams &a, const char *rows, const uint8_t *mask, uint64_t t,
+                                           int e0, float (&z)[VPL]) {
+  if (t < a.tokens && (mask == nullptr || mask[t] != 0)) {
+    load_row<T, VPL>(rows + t * (uint64_t)a.E * T::kBytes, e0, a.E, a.vec, z);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) z[j] = -INFINITY;
+  }
+}
+
 template <int LPT>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -82,210 +104,344 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// The numbers' order as unsigned integers; 0 for -inf and NaN, which are never
-// chosen.  -0 counts as +0, so that the two tie.
-__device__ __forceinline__ uint32_t order_key(float z) {
-  if (!(z > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(z + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+// The largest value of the LPT lanes that share a row (no NaN).
+template <int LPT>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (LPT == 32) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+  } else {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+  }
 }
 
-// exp(z - max) of this lane's values, and the row's sum of them; a row of -inf
-// alone (max = -inf) is all zeros.  A NaN, or +inf, makes the sum NaN.
+// exp(z - m) as 2^((z - m) log2 e); the difference is exact where it matters
+// (z near m).  ex2.approx is within 2 units in the last place.
+__device__ __forceinline__ float exp_diff(float z, float m) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((z - m) * kLog2e));
+  return y;
+}
+__device__ __forceinline__ float reciprocal(float x) {  // within one unit in the last place
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What a row is without the experts that can't be chosen: NaN becomes -inf.
+__device__ __forceinline__ float choosable(float z) { return fmaxf(z, -INFINITY); }
+
+// ex = exp(z - top) of this lane's values, and the row's sum of them; `top` is
+// the row's largest number (-inf: it has none).  A row of -inf alone is not
+// live, and zero; a NaN, or +inf, makes the sum NaN.
 template <int LPT, int VPL>
-__device__ __forceinline__ float row_exp(const float (&z)[VPL], float (&ex)[VPL], bool *live) {
-  float m = -INFINITY;
-  int nan = 0;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    m = fmaxf(m, z[j]);
-    nan |= isnan(z[j]) ? 1 : 0;
-  }
-  // every lane takes part in every shuffle, whatever it holds
-#pragma unroll
-  for (int d = LPT / 2; d > 0; d >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    nan |= __shfl_xor_sync(0xffffffffu, nan, d);
-  }
-  *live = m > -INFINITY || nan != 0;
-  const float base = m > -INFINITY ? m : 0.0f;
+__device__ __forceinline__ float row_exp(const float (&z)[VPL], float top, float (&ex)[VPL], bool *live) {
+  const float base = top > -INFINITY ? top : 0.0f;
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    ex[j] = expf(z[j] - base);
+    ex[j] = exp_diff(z[j], base);
     s += ex[j];
   }
-  return row_sum<LPT>(s);
+  s = row_sum<LPT>(s);
+  *live = top > -INFINITY || isnan(s);
+  return s;
 }
+
+// What a block holds of its tokens: each expert's probabilities (a lane's
+// experts) and choices (in shared memory, added by the lanes that win them).
+template <int VPL>
+struct Sums {
+  float p[VPL];
+  int32_t tokens;
+};
+
+template <int LPT>
+struct Slots {  // the chosen experts of the tokens that a warp is at
+  static constexpr int kSlots = LPT == 1 ? 8 : kMaxK;  // 8 experts at most have a lane per token
+  int32_t id[32 / LPT][kSlots];
+  float z[32 / LPT][kSlots];
+};
+
+// The tokens of rank r that fall to this block.
+template <class T, int LPT, int VPL>
+__device__ __forceinline__ void walk(const GateParams &a, int r, int block, int blocks, Slots<LPT> &slots,
+                                     int32_t *count, Sums<VPL> &sum) {
+  constexpr int TPW = 32 / LPT;  // tokens per warp and step
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane & (LPT - 1), grp = lane / LPT, e0 = sub * VPL;
+  const uint32_t grp_mask = LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1u) << (grp * LPT);
+  const uint64_t step = (uint64_t)blocks * kWarps * TPW;
+  const char *rows = a.z[r];
+  const uint8_t *mask = a.mask[r];
+  int32_t *ids = a.ids[r];
+  float *weights = a.w[r];
+  const int k = a.k;
+  uint64_t t = ((uint64_t)block * kWarps + warp) * TPW + grp;
+  float next[VPL];
+  load_token<T, VPL>(a, rows, mask, t, e0, next);
+  for (; t - grp < a.tokens; t += step) {
+    const bool have = t < a.tokens;
+    float z[VPL], ex[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) z[j] = next[j];
+    load_token<T, VPL>(a, rows, mask, t + step, e0, next);  // in flight while this one is worked on
+    // the lane's two best, the lower index first among equals
+    float b1 = choosable(z[0]), b2 = -INFINITY;
+    int j1 = 0, j2 = 0;
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) {
+      const float v = choosable(z[j]);
+      const bool first = v > b1, second = v > b2;
+      b2 = first ? b1 : second ? v : b2;
+      j2 = first ? j1 : second ? j : j2;
+      b1 = first ? v : b1;
+      j1 = first ? j : j1;
+    }
+    float best = row_max<LPT>(b1);
+    const float top = best;
+    bool live;
+    const float total = row_exp<LPT, VPL>(z, top, ex, &live);
+    const float inv = live ? reciprocal(total) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) sum.p[j] = fmaf(ex[j], inv, sum.p[j]);
+    sum.tokens += (live && sub == 0) ? 1 : 0;
+    uint32_t sel = 0;
+    for (int i = 0; i < k; ++i) {
+      if (i > 0) best = row_max<LPT>(b1);
+      const uint32_t who = __ballot_sync(0xffffffffu, b1 == best) & grp_mask;
+      const bool win = lane == __ffs(who) - 1;
+      if (win) {
+        const bool found = best > -INFINITY;
+        slots.id[grp][i] = found ? e0 + j1 : -1;
+        slots.z[grp][i] = best;
+        if (found) atomicAdd(&count[e0 + j1], 1);  // integers: any order gives the same sum
+        sel |= 1u << j1;
+        b1 = b2;
+        j1 = j2;
+        b2 = -INFINITY;
+      }
+      // a lane that has spent both looks for its next best two
+      const bool spent = win && b1 == -INFINITY && i + 1 < k;
+      if (__any_sync(0xffffffffu, spent)) {
+        if (spent) {
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) {
+            const float v = (sel >> j) & 1u ? -INFINITY : choosable(z[j]);
+            const bool first = v > b1, second = v > b2;
+            b2 = first ? b1 : second ? v : b2;
+            j2 = first ? j1 : second ? j : j2;
+            b1 = first ? v : b1;
+            j1 = first ? j : j1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    // slot i is lane i % LPT's: its weight, and the chosen weights' sum
+    float share = 1.0f;
+    if (a.norm) {
+      float s = 0.0f;
+      for (int i = sub; i < k; i += LPT)
+        if (slots.id[grp][i] >= 0) s += exp_diff(slots.z[grp][i], top);
+      share = row_sum<LPT>(s);
+    }
+    const float per = a.norm ? reciprocal(share) : inv;
+    if (have) {
+      for (int i = sub; i < k; i += LPT) {
+        const int id = slots.id[grp][i];
+        ids[t * k + i] = id;
+        // (inv carries the NaN of a row that holds one)
+        weights[t * k + i] = id < 0 ? 0.0f : a.norm && !isnan(inv) ? exp_diff(slots.z[grp][i], top) * per
+                                                                  : exp_diff(slots.z[grp][i], top) * inv;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Adds up what the block's lanes and warps hold: expert e's sum of
+// probabilities goes to thread e % kNT's calls of `take(e, p)`, and the number
+// of tokens to every thread.  Ends with a barrier.
+template <int LPT, int VPL, class Take>
+__device__ __forceinline__ int32_t gather_block(Sums<VPL> &sum, float (&buf)[kWarps][LPT * VPL],
+                                                int32_t (&tok)[kWarps], int E, Take take) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+#pragma unroll
+    for (int d = 16; d >= LPT; d >>= 1) sum.p[j] += __shfl_xor_sync(0xffffffffu, sum.p[j], d);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum.tokens += __shfl_xor_sync(0xffffffffu, sum.tokens, d);
+  if (lane == 0) tok[warp] = sum.tokens;
+  if (lane < LPT) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) buf[warp][lane * VPL + j] = sum.p[j];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kNT) {
+    float p = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) p += buf[w][e];
+    take(e, p);
+  }
+  int32_t tokens = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) tokens += tok[w];
+  __syncthreads();
+  return tokens;
+}
+
+template <int VPL>
+__device__ __forceinline__ void clear(Sums<VPL> &sum, int32_t *count, int n) {
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) sum.p[j] = 0.0f;
+  sum.tokens = 0;
+  for (int e = threadIdx.x; e < n; e += kNT) count[e] = 0;
+  __syncthreads();
+}
+
+__device__ __forceinline__ float warp_sum(float v) { return row_sum<32>(v); }
 
 template <class T, int LPT, int VPL>
 __global__ void __launch_bounds__(kNT) rc_gate_kernel(const __grid_constant__ GateParams a) {
-  constexpr int TPW = 32 / LPT;  // tokens per warp and step
-  __shared__ float sp[kWarps][LPT * VPL];
-  __shared__ int32_t sc[kWarps][LPT * VPL];
-  __shared__ int32_t sm[kWarps];
+  __shared__ float buf[kWarps][LPT * VPL];
+  __shared__ Slots<LPT> slots[kWarps];
+  __shared__ int32_t tok[kWarps], count[LPT * VPL];
+  Sums<VPL> sum;
+  clear(sum, count, LPT * VPL);
   pdl_wait();
-  const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane & (LPT - 1), e0 = sub * VPL;
-  float acc[VPL];
-  int32_t cnt[VPL];
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    acc[j] = 0.0f;
-    cnt[j] = 0;
+  walk<T, LPT, VPL>(a, blockIdx.y, blockIdx.x, gridDim.x, slots[threadIdx.x >> 5], count, sum);
+  const uint64_t b = (uint64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int32_t tokens = gather_block<LPT>(sum, buf, tok, a.E, [&](int e, float p) {
+    a.part[b * a.E + e] = make_float2(p, __int_as_float(count[e]));
+  });
+  if (threadIdx.x == 0) a.part_m[b] = tokens;
+}
+
+// Few tokens: one block walks all ranks and finishes by itself.
+template <class T, int LPT, int VPL>
+__global__ void __launch_bounds__(kNT) rc_gate_one_kernel(const __grid_constant__ GateParams a) {
+  __shared__ float buf[kWarps][LPT * VPL];
+  __shared__ Slots<LPT> slots[kWarps];
+  __shared__ int32_t tok[kWarps], count[LPT * VPL];
+  __shared__ float total_p[LPT * VPL], dots[kWarps];
+  __shared__ int32_t total_c[LPT * VPL];
+  pdl_wait();
+  int32_t m = 0;
+  for (int r = 0; r < a.p; ++r) {
+    Sums<VPL> sum;
+    clear(sum, count, LPT * VPL);
+    walk<T, LPT, VPL>(a, r, 0, 1, slots[threadIdx.x >> 5], count, sum);
+    m += gather_block<LPT>(sum, buf, tok, a.E, [&](int e, float p) {  // thread e % kNT only
+      const int32_t c = count[e];
+      a.counts[r][e] = c;
+      total_p[e] = r == 0 ? p : total_p[e] + p;
+      total_c[e] = r == 0 ? c : total_c[e] + c;
+    });
   }
-  int32_t tokens = 0;
-  const uint64_t step = (uint64_t)gridDim.x * kWarps * TPW;
-  for (uint64_t t0 = ((uint64_t)blockIdx.x * kWarps + warp) * TPW; t0 < a.tokens; t0 += step) {
-    const uint64_t t = t0 + lane / LPT;
-    const bool have = t < a.tokens;
-    const bool unmasked = have && (a.mask[r] == nullptr || a.mask[r][t] != 0);
-    float z[VPL], ex[VPL];
-    if (unmasked) {
-      load_row<T, VPL>(a.z[r] + t * (uint64_t)a.E * T::kBytes, e0, a.E, a.vec, z);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) z[j] = -INFINITY;
-    }
-    bool live;
-    const float total = row_exp<LPT, VPL>(z, ex, &live);
-    const float inv = live ? 1.0f / total : 0.0f;
-    uint32_t key[VPL];
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      key[j] = order_key(z[j]);
-      ex[j] *= inv;  // the probability
-      acc[j] += ex[j];
-    }
-    tokens += (live && sub == 0) ? 1 : 0;
-    // k rounds: the lane's best (lowest index first), then the row's best
-    float share = 0.0f;
-    for (int i = 0; i < a.k; ++i) {
-      uint32_t bk = 0;
-      int bj = 0;
-      float bp = 0.0f;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        if (key[j] > bk) {
-          bk = key[j];
-          bj = j;
-          bp = ex[j];
-        }
-      }
-      int be = e0 + bj;
-#pragma unroll
-      for (int d = LPT / 2; d > 0; d >>= 1) {
-        const uint32_t ok = __shfl_xor_sync(0xffffffffu, bk, d);
-        const int oe = __shfl_xor_sync(0xffffffffu, be, d);
-        const float op = __shfl_xor_sync(0xffffffffu, bp, d);
-        if (ok > bk || (ok == bk && oe < be)) {
-          bk = ok;
-          be = oe;
-          bp = op;
-        }
-      }
-      const bool found = bk != 0;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        if (found && be == e0 + j) {
-          key[j] = 0;
-          cnt[j] += 1;
-        }
-      }
-      share += found ? bp : 0.0f;
-      // lane i % LPT writes slot i
-      if (have && (i & (LPT - 1)) == sub) {
-        a.ids[r][t * a.k + i] = found ? be : -1;
-        a.w[r][t * a.k + i] = found ? bp : 0.0f;
-      }
-    }
-    if (a.norm && have) {
-      // the same lane that wrote the slot scales it
-      for (int i = sub; i < a.k; i += LPT) {
-        const float v = a.w[r][t * a.k + i];
-        a.w[r][t * a.k + i] = share > 0.0f || isnan(share) ? v / share : 0.0f;
-      }
-    }
-  }
-  // lanes that own the same experts, then the block's warps
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-#pragma unroll
-    for (int d = 16; d >= LPT; d >>= 1) {
-      acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], d);
-      cnt[j] += __shfl_xor_sync(0xffffffffu, cnt[j], d);
-    }
-    if (lane < LPT) {
-      sp[warp][e0 + j] = acc[j];
-      sc[warp][e0 + j] = cnt[j];
-    }
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, d);
-  if (lane == 0) sm[warp] = tokens;
-  __syncthreads();
-  const uint64_t b = (uint64_t)r * gridDim.x + blockIdx.x;
+  const float M = (float)m, per = fmaxf(M, 1.0f);
+  float dot = 0.0f;
   for (int e = threadIdx.x; e < a.E; e += kNT) {
-    float s = 0.0f;
-    int32_t c = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      s += sp[w][e];
-      c += sc[w][e];
-    }
-    a.part_p[b * a.E + e] = s;
-    a.part_c[b * a.E + e] = c;
+    const float f = (float)total_c[e] / ((float)a.k * per), mean = total_p[e] / per;
+    a.stats[e] = f;
+    a.stats[a.E + e] = mean;
+    dot += f * mean;
   }
+  dot = warp_sum(dot);
+  if ((threadIdx.x & 31) == 0) dots[threadIdx.x >> 5] = dot;
+  __syncthreads();
   if (threadIdx.x == 0) {
-    int32_t m = 0;
-    for (int w = 0; w < kWarps; ++w) m += sm[w];
-    a.part_m[b] = m;
+    float s = 0.0f;
+    for (int w = 0; w < kWarps; ++w) s += dots[w];
+    a.stats[2 * a.E] = M;
+    a.loss[0] = a.coef * (float)a.E * s;
   }
 }
 
-// Adds the blocks' partials in block order: one block, one thread per expert.
-__global__ void __launch_bounds__(1024) rc_gate_stats_kernel(const __grid_constant__ GateParams a) {
-  __shared__ float red[32];
-  __shared__ int64_t tot[32];
-  pdl_wait();
+// Adds the blocks' partials in block order.  A cluster of kStatBlocks blocks,
+// each `span` neighbouring experts (a power of two); within a block, 256 /
+// span groups of threads share the partials.
+__global__ void __cluster_dims__(kStatBlocks, 1, 1) __launch_bounds__(256)
+    rc_gate_stats_kernel(const __grid_constant__ GateParams a, int span) {
+  __shared__ float sp[256];
+  __shared__ int32_t sc[kMaxRanks][64];
+  __shared__ int64_t tot[8];
+  __shared__ float red[8], dots[kStatBlocks];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = threadIdx.x & (span - 1), g = threadIdx.x / span, groups = 256 / span;
+  const int e = blockIdx.x * span + col;
+  for (int i = threadIdx.x; i < kMaxRanks * 64; i += 256) sc[i / 64][i % 64] = 0;
+  __syncthreads();
+  pdl_wait();
   int64_t m = 0;
-  for (int b = threadIdx.x; b < a.p * a.blocks; b += blockDim.x) m += a.part_m[b];
+  for (int b = threadIdx.x; b < a.p * a.blocks; b += 256) m += a.part_m[b];
+  float s = 0.0f;
+  if (e < a.E) {
+    constexpr int kIn = 8;  // loads in flight
+    const int rows = a.p * a.blocks;
+    for (int b0 = g; b0 < rows; b0 += kIn * groups) {
+      float2 v[kIn];
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) {
+        const int b = b0 + i * groups;
+        v[i] = b < rows ? a.part[(uint64_t)b * a.E + e] : make_float2(0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) {
+        s += v[i].x;
+        const int c = __float_as_int(v[i].y);
+        if (c) atomicAdd(&sc[(b0 + i * groups) / a.blocks][col], c);  // integers: any order gives the same sum
+      }
+    }
+  }
+  sp[threadIdx.x] = s;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m += __shfl_xor_sync(0xffffffffu, m, d);
   if (lane == 0) tot[warp] = m;
   __syncthreads();
   m = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) m += tot[w];
-  const float M = (float)m, inv = 1.0f / fmaxf(M, 1.0f);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m += tot[w];
+  const float M = (float)m, per = fmaxf(M, 1.0f);
   float dot = 0.0f;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    float s = 0.0f;
+  if (g == 0 && e < a.E) {
+    s = 0.0f;
+    for (int q = 0; q < groups; ++q) s += sp[q * span + col];
     int64_t c = 0;
     for (int r = 0; r < a.p; ++r) {
-      int32_t cr = 0;
-      for (int b = 0; b < a.blocks; ++b) {
-        const uint64_t at = ((uint64_t)r * a.blocks + b) * a.E + e;
-        s += a.part_p[at];
-        cr += a.part_c[at];
-      }
-      a.counts[r][e] = cr;
-      c += cr;
+      a.counts[r][e] = sc[r][col];
+      c += sc[r][col];
     }
-    const float f = (float)c / ((float)a.k * fmaxf(M, 1.0f)), mean = s * inv;
+    const float f = (float)c / ((float)a.k * per), mean = s / per;
     a.stats[e] = f;
     a.stats[a.E + e] = mean;
-    dot += f * mean;
+    dot = f * mean;
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+  dot = warp_sum(dot);
   if (lane == 0) red[warp] = dot;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float s = 0.0f;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
+    dot = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) dot += red[w];
+    // into the first block's shared memory
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(smem_addr(&dots[blockIdx.x])));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(dot) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kStatBlocks; ++w) sum += dots[w];
     a.stats[2 * a.E] = M;
-    a.loss[0] = a.coef * (float)a.E * s;
+    a.loss[0] = a.coef * (float)a.E * sum;
   }
 }
 
@@ -293,75 +449,95 @@ __global__ void __launch_bounds__(1024) rc_gate_stats_kernel(const __grid_consta
 // experts' probabilities, and q_i = p_i / S (normalised) or p_i:
 //   dz = p (a - sum p a) + [chosen] q dw - (normalised: [chosen] q, else p) * sum_i q_i dw_i
 template <class T, int LPT, int VPL>
-__global__ void __launch_bounds__(kNT) rc_gate_backward_kernel(const __grid_constant__ GateParams a) {
+__global__ void __launch_bounds__(kBackNT) rc_gate_backward_kernel(const __grid_constant__ GateParams a) {
   constexpr int TPW = 32 / LPT;
   constexpr int V = kVec<T>;
+  constexpr uint32_t kNone = 0x7fffffffu;  // marks experts that were not chosen
+  constexpr int kBackWarps = kBackNT / 32;
+  __shared__ __align__(16) uint32_t grad[kBackWarps][32 * VPL];  // gradients of the chosen weights, by expert
   pdl_wait();
   const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane & (LPT - 1), e0 = sub * VPL;
+  const int sub = lane & (LPT - 1), grp = lane / LPT, e0 = sub * VPL;
+  uint32_t *row_grad = grad[warp] + grp * (LPT * VPL);
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) row_grad[e0 + j] = kNone;
   const float M = a.stats[2 * a.E];
   const float c = a.dloss ? a.dloss[0] * a.coef * (float)a.E / fmaxf(M, 1.0f) : 0.0f;
   float slope[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) slope[j] = e0 + j < a.E ? c * a.stats[e0 + j] : 0.0f;
-  const uint64_t step = (uint64_t)gridDim.x * kWarps * TPW;
-  for (uint64_t t0 = ((uint64_t)blockIdx.x * kWarps + warp) * TPW; t0 < a.tokens; t0 += step) {
-    const uint64_t t = t0 + lane / LPT;
+  const uint64_t step = (uint64_t)gridDim.x * kBackWarps * TPW;
+  const char *rows = a.z[r];
+  const uint8_t *mask = a.mask[r];
+  const int32_t *ids = a.ids[r];
+  const float *dw = a.dw[r];
+  char *dz = a.dz[r];
+  const int k = a.k;
+  uint64_t t = ((uint64_t)blockIdx.x * kBackWarps + warp) * TPW + grp;
+  float next[VPL];
+  load_token<T, VPL>(a, rows, mask, t, e0, next);
+  for (; t - grp < a.tokens; t += step) {
     const bool have = t < a.tokens;
-    const bool unmasked = have && (a.mask[r] == nullptr || a.mask[r][t] != 0);
-    const char *row = a.z[r] + t * (uint64_t)a.E * T::kBytes;
-    float z[VPL], p[VPL], g[VPL];
-    uint32_t sel = 0;
-    if (unmasked) {
-      load_row<T, VPL>(row, e0, a.E, a.vec, z);
-    } else {
+    float z[VPL], p[VPL];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) z[j] = -INFINITY;
-    }
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) g[j] = 0.0f;
-    if (unmasked && a.dw[r]) {
-      for (int i = 0; i < a.k; ++i) {
-        const int id = a.ids[r][t * a.k + i];
-        const float d = a.dw[r][t * a.k + i];
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-          if (id == e0 + j) {
-            sel |= 1u << j;
-            g[j] = d;
-          }
-        }
+    for (int j = 0; j < VPL; ++j) z[j] = next[j];
+    __syncwarp();
+    if (have && dw != nullptr) {  // (a masked token's ids are -1)
+      for (int i = sub; i < k; i += LPT) {
+        const int id = ids[t * k + i];
+        if (id >= 0 && id < a.E) row_grad[id] = __float_as_uint(dw[t * k + i]);
       }
     }
+    load_token<T, VPL>(a, rows, mask, t + step, e0, next);  // in flight while this one is worked on
+    float top = choosable(z[0]);
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) top = fmaxf(top, z[j]);
+    top = row_max<LPT>(top);
     bool live;
-    const float total = row_exp<LPT, VPL>(z, p, &live);
-    const float inv = live ? 1.0f / total : 0.0f;
+    const float total = row_exp<LPT, VPL>(z, top, p, &live);
+    const float inv = live ? reciprocal(total) : 0.0f;
+    __syncwarp();
+    uint32_t g[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; j += 4) {
+      const uint4 q = *reinterpret_cast<const uint4 *>(row_grad + e0 + j);
+      g[j] = q.x;
+      g[j + 1] = q.y;
+      g[j + 2] = q.z;
+      g[j + 3] = q.w;
+    }
+    __syncwarp();
     float pa = 0.0f, ps = 0.0f, pd = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       p[j] *= inv;
-      pa += p[j] * slope[j];
-      ps += (sel >> j) & 1u ? p[j] : 0.0f;
-      pd += p[j] * g[j];
+      const bool s = g[j] != kNone;
+      if (s) row_grad[e0 + j] = kNone;
+      const float d = s ? __uint_as_float(g[j]) : 0.0f;
+      pa = fmaf(p[j], slope[j], pa);
+      ps += s ? p[j] : 0.0f;
+      pd = fmaf(p[j], d, pd);
     }
     pa = row_sum<LPT>(pa);
     ps = row_sum<LPT>(ps);
     pd = row_sum<LPT>(pd);
-    const float q = a.norm ? (ps > 0.0f ? 1.0f / ps : 0.0f) : 1.0f;
-    const float inner = pd * q;
+    if (a.norm) {
+      const float q = ps > 0.0f ? reciprocal(ps) : 0.0f, inner = pd * q;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const bool s = (sel >> j) & 1u;
-      float d = p[j] * (slope[j] - pa);
-      if (a.norm) {
-        if (s) d += p[j] * q * (g[j] - inner);
-      } else {
-        d += p[j] * ((s ? g[j] : 0.0f) - inner);
+      for (int j = 0; j < VPL; ++j) {
+        const float d = g[j] != kNone ? (__uint_as_float(g[j]) - inner) * q : 0.0f;
+        z[j] = live ? p[j] * ((slope[j] - pa) + d) : 0.0f;
       }
-      z[j] = live ? d : 0.0f;
+    } else {
+      const float both = pa + pd;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const float d = g[j] != kNone ? __uint_as_float(g[j]) : 0.0f;
+        z[j] = live ? p[j] * ((slope[j] + d) - both) : 0.0f;
+      }
     }
     if (!have) continue;
-    char *out = a.dz[r] + t * (uint64_t)a.E * T::kBytes;
+    char *out = dz + t * (uint64_t)a.E * T::kBytes;
     if (a.vec) {
 #pragma unroll
       for (int j = 0; j < VPL; j += V) {
@@ -369,7 +545,7 @@ __global__ void __launch_bounds__(kNT) rc_gate_backward_kernel(const __grid_cons
           float o[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) o[i] = z[j + i];
-          store_vec<T, V>(out + (uint64_t)(e0 + j) * T::kBytes, o);
+          store_vec<T, V, true>(out + (uint64_t)(e0 + j) * T::kBytes, o);
         }
       }
     } else {
@@ -380,26 +556,30 @@ __global__ void __launch_bounds__(kNT) rc_gate_backward_kernel(const __grid_cons
   }
 }
 
-// Blocks per rank: enough for the machine, at most one step of tokens each.
-int blocks_per_rank(uint64_t tokens, int tpw, int p) {
-  const uint64_t want = (tokens + (uint64_t)kWarps * tpw - 1) / ((uint64_t)kWarps * tpw);
-  const uint64_t most = std::max(1, device_sm_count() * 2 / p);
-  return (int)std::max<uint64_t>(1, std::min(want, most));
+// Blocks of `warps` warps per rank: all tokens in one step each, but no more
+// than `most` over the ranks.
+int blocks_per_rank(uint64_t tokens, int per_block, int p, int most) {
+  const uint64_t want = (tokens + per_block - 1) / per_block;
+  return (int)std::max<uint64_t>(1, std::min<uint64_t>(want, std::max(1, most / p)));
 }
 
 template <class T, int LPT, int VPL>
 cudaError_t run(const GateJob &job, GateParams &a, cudaStream_t s) {
+  constexpr int TPW = 32 / LPT;
   cudaError_t err;
   if (job.backward) {
-    const int blocks = blocks_per_rank(job.tokens, 32 / LPT, std::max(1, job.p / 4));
-    return launch_kernel(rc_gate_backward_kernel<T, LPT, VPL>, dim3(blocks, job.p), dim3(kNT), 0, s, a);
+    const int blocks = blocks_per_rank(job.tokens, kBackNT / 32 * TPW, job.p, device_sm_count() * 8);
+    return launch_kernel(rc_gate_backward_kernel<T, LPT, VPL>, dim3(blocks, job.p), dim3(kBackNT), 0, s, a);
   }
-  a.blocks = blocks_per_rank(job.tokens, 32 / LPT, job.p);
-  if (a.blocks > gate_max_blocks(job.p)) return cudaErrorInvalidValue;
+  // one block's time for a rank's tokens in one step is about the second launch's
+  if (job.tokens <= (uint64_t)kWarps * TPW && job.p <= 2)
+    return launch_kernel(rc_gate_one_kernel<T, LPT, VPL>, dim3(1), dim3(kNT), 0, s, a);
+  a.blocks = blocks_per_rank(job.tokens, kWarps * TPW, job.p, device_sm_count() * 2);
   if ((err = launch_kernel(rc_gate_kernel<T, LPT, VPL>, dim3(a.blocks, job.p), dim3(kNT), 0, s, a)) != cudaSuccess)
     return err;
-  const int nt = std::min(1024, (job.experts + 31) / 32 * 32);
-  return launch_kernel(rc_gate_stats_kernel, dim3(1), dim3(nt), 0, s, a);
+  int span = 1;
+  while (span * kStatBlocks < job.experts) span *= 2;
+  return launch_kernel(rc_gate_stats_kernel, dim3(kStatBlocks), dim3(256), 0, s, a, span);
 }
 
 // Lanes per token: the fewest that hold the row at 8 values each, so that
@@ -446,9 +626,8 @@ cudaError_t launch_gate(const GateJob &job, cudaStream_t s) {
   a.norm = job.normalize;
   if (!job.backward) {
     const uint64_t rows = (uint64_t)gate_max_blocks(job.p) * job.p;
-    a.part_p = static_cast<float *>(job.ws);
-    a.part_c = reinterpret_cast<int32_t *>(a.part_p + rows * job.experts);
-    a.part_m = a.part_c + rows * job.experts;
+    a.part = static_cast<float2 *>(job.ws);
+    a.part_m = reinterpret_cast<int32_t *>(a.part + rows * job.experts);
   }
   if (job.dt == kF32) return by_experts<F32>(job, a, s);
   if (job.dt == kBF16) return by_experts<BF16>(job, a, s);

@@ -24,6 +24,7 @@
 // gradient and its rounding would show in every output of the row; there G is
 // kept as the sum of two bf16 planes (2^-17).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -38,18 +39,30 @@ __device__ unsigned int g_wait_timeouts_ce = 0;
 
 namespace {
 
-constexpr int kNT = 256;       // copy warp, product warp, two idle, four epilogue warps
-constexpr int kBM = 128;       // rows of a tile (tensor-memory lanes)
-constexpr int kBN = 256;       // columns of a tile
+// A pair of blocks makes one 256 x 256 tile, 64 wide steps of k: block c stages
+// rows [128 c, 128 c + 128) of A and of B and keeps rows [128 c, ...) of the
+// result in its tensor memory.  Warps: sixteen for the epilogue (32 rows x 64
+// columns each, which fit their registers), one for the copies, one for the
+// products.
+constexpr int kEpiWarps = 16;
+constexpr int kNT = 32 * (kEpiWarps + 2);
+constexpr int kBM = 256;       // rows of a pair's tile
+constexpr int kBN = 256;       // columns
+constexpr int kHalf = 128;     // a block's share of either
 constexpr int kBK = 64;        // one 128-byte row of bf16
-constexpr int kStages = 4;
-constexpr uint32_t kABytes = kBM * kBK * 2;
-constexpr uint32_t kBBytes = kBN * kBK * 2;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024;  // + slack to align to 1024
-constexpr int kGroupM = 16;    // row tiles that share a sweep over the columns (L2 reuse)
+constexpr uint32_t kOpBytes = kHalf * kBK * 2;       // 16 KiB of either operand per block and stage
+constexpr uint32_t kStageBytes = 2 * kOpBytes;
+constexpr uint32_t kBoxBytes = 4096;                 // an epilogue warp's staging: 32 rows of 128 bytes
+constexpr int kGroupM = 8;     // row tiles that share a sweep over the columns (L2 reuse)
+// The tensor cores add to their fp32 accumulators by truncation, which pulls
+// a long sum towards zero by about 2^-24 per step.  The logits are therefore
+// summed in chunks of 512 products; the chunks are added in registers with
+// ordinary rounding.  (4096-wide, 2048 tokens: the loss is 4e-7 off its 64-bit
+// value instead of 2.2e-6.)
+constexpr int kChunk = 8;      // steps of k per chunk
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256;  // of the small kernels
 
 enum Mode : int {
   kStats = 0,  // z tile -> (max, sum exp) per row, target logit
@@ -58,29 +71,32 @@ enum Mode : int {
   kDH = 3,     // G W -> fp32 sums
 };
 
+constexpr int stages(int mode) { return mode == kStats ? 6 : 5; }
+constexpr uint32_t smem_bytes(int mode) {  // + slack to align to 1024
+  return stages(mode) * kStageBytes + (mode == kStats ? 0u : kEpiWarps * kBoxBytes) + 1024u;
+}
+
 struct alignas(64) CeParams {
   CUtensorMap a;              // kStats, kGrad: h (K-major); kDW: G (64 x 64 boxes); kDH: G (K-major)
   CUtensorMap b[kMaxRanks];   // kStats, kGrad: W_r (K-major); kDW: h (64 x 64 boxes, b[0]); kDH: W_r (64 x 64 boxes)
+  CUtensorMap out[kMaxRanks]; // kGrad: G (out[0]); kDW: dW_r; kDH: the sums (out[0])
   int rows[kMaxRanks];        // rows of each rank's piece
-  char *dw[kMaxRanks];        // kDW
+  char *dw[kMaxRanks];        // kDW without dw_tma
   const int32_t *target;
   const float *lse_in, *dloss;  // kGrad
   float2 *part;               // kStats: [tile][N]
   float *ztarget;             // kStats: [N]
-  char *g;                    // kGrad: [planes][N][gcols] bf16
-  float *dh;                  // kDH: [splits][N][dpad]
-  int64_t N, V;
-  int D, dpad;
+  int N, V;
+  int D;
   int C;                      // rows of a full rank piece
   int tpr;                    // 256-row tiles per rank
   int j0;                     // first tile of this launch's piece
-  int gcols;                  // columns of G (the piece's, a multiple of 256)
   int planes;                 // bf16 planes of G
   int mt, nt, nk, kper, splits;
-  int64_t tiles;
+  uint32_t tiles;
   int ignore;
   bool first;                 // kDH: store instead of add
-  bool dw_vec;                // kDW: rows can be written as 16-byte vectors
+  bool dw_tma;                // kDW: rows are 16-byte multiples at 16-byte bases
 };
 
 struct TileAt {
@@ -89,17 +105,16 @@ struct TileAt {
 
 // Tiles go in groups of kGroupM row tiles, all columns of a group before the
 // next group; the splits of k are outermost.
-__device__ __forceinline__ TileAt tile_at(const CeParams &a, int64_t t) {
-  const int64_t per = (int64_t)a.mt * a.nt;
+__device__ __forceinline__ TileAt tile_at(const CeParams &a, uint32_t t) {
+  const uint32_t per = (uint32_t)a.mt * a.nt, gsz = (uint32_t)kGroupM * a.nt;
   TileAt r;
   r.s = (int)(t / per);
-  const int64_t u = t - r.s * per;
-  const int64_t gsz = (int64_t)kGroupM * a.nt;
-  const int g = (int)(u / gsz);
-  const int64_t w = u - g * gsz;
-  const int gm = min(kGroupM, a.mt - g * kGroupM);
-  r.n = (int)(w / gm);
-  r.m = g * kGroupM + (int)(w - (int64_t)r.n * gm);
+  t -= r.s * per;
+  const uint32_t g = t / gsz;
+  t -= g * gsz;
+  const uint32_t gm = min((uint32_t)kGroupM, a.mt - g * kGroupM);
+  r.n = (int)(t / gm);
+  r.m = (int)(g * kGroupM + (t - r.n * gm));
   return r;
 }
 
@@ -112,9 +127,9 @@ __device__ __forceinline__ float ex2(float x) {
 struct Flow {
   volatile uint32_t *dead;
   __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_cluster(bar, parity)) {
       if (*dead) return false;
       if (global_ns() - t0 > kWaitLimitNs) {
         if (atomicExch(const_cast<uint32_t *>(dead), 1u) == 0) atomicAdd(&g_wait_timeouts_ce, 1u);
@@ -125,113 +140,145 @@ struct Flow {
   }
 };
 
+// Before a warp writes its staging rows: its last copy out has read them.
+__device__ __forceinline__ void staging_free(int lane) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+}
+// After it wrote them: visible to the copy engine.
+__device__ __forceinline__ void staging_ready() {
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+// 16-byte unit u of this lane's 128-byte row, in the 128-byte swizzle.
+__device__ __forceinline__ uint32_t staging_unit(uint32_t box, int lane, int u) {
+  return box + lane * 128 + ((u ^ (lane & 7)) << 4);
+}
+
 template <int MODE>
-__global__ void __launch_bounds__(kNT, 1) rc_ce_gemm_kernel(const __grid_constant__ CeParams a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
+    rc_ce_gemm_kernel(const __grid_constant__ CeParams a) {
   constexpr bool A_MN = MODE == kDW;
   constexpr bool B_MN = MODE == kDW || MODE == kDH;
+  constexpr bool LOGITS = MODE == kStats || MODE == kGrad;
+  constexpr uint32_t S = stages(MODE);
   extern __shared__ char smem_raw[];
-  __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  __shared__ uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base_s;
   __shared__ uint32_t dead_s;
+  __shared__ float2 join[MODE == kStats ? 4 : 1][kHalf];
+  __shared__ uint64_t joined[4], join_free[4];  // kStats, per 32 rows
   const uint32_t smem0 = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t c = cluster_rank();
+  const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (uint32_t i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 128);
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&joined[i], 4);
+      mbar_init(&join_free[i], 1);
     }
     mbar_init(&drained, 1);
     dead_s = 0;
     mbar_init_fence();
   }
-  if (warp == 2) tmem_alloc_all(&tmem_base_s);
+  if (warp == kEpiWarps + 1) tmem_alloc_all(&tmem_base_s);
   tc_fence_before_sync();
   __syncthreads();
+  cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_base_s;
   const Flow flow{&dead_s};
   pdl_wait();
 
-  if (warp == 0) {
+  if (warp == kEpiWarps) {
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
+      for (uint32_t t = pair; ok && t < a.tiles; t += pairs) {
         const TileAt w = tile_at(a, t);
         const int k0 = w.s * a.kper, k1 = min(a.nk, k0 + a.kper);
         for (int k = k0; k < k1; ++k, ++it) {
-          const uint32_t slot = it % kStages;
-          if (it >= kStages && !flow.wait(&empty[slot], (it / kStages - 1) & 1)) {
+          const uint32_t slot = it % S;
+          if (it >= S && !flow.wait(&empty[slot], (it / S - 1) & 1)) {
             ok = false;
             break;
           }
-          const uint32_t sa = smem0 + slot * kStageBytes, sb = sa + kABytes;
-          mbar_arrive_expect_tx(&full[slot], kStageBytes);
-          if constexpr (MODE == kStats || MODE == kGrad) {
+          const uint32_t sa = smem0 + slot * kStageBytes, sb = sa + kOpBytes;
+          // both blocks' bytes are counted on the first block's barrier
+          if (c == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStageBytes);
+          const uint32_t bar = first_block_addr(&full[slot]);
+          const int am = w.m * kBM + (int)c * kHalf, bn = w.n * kBN + (int)c * kHalf;
+          if constexpr (LOGITS) {
             const int j = a.j0 + w.n, r = j / a.tpr;
-            tma_load_2d(sa, &a.a, k * kBK, w.m * kBM, &full[slot]);
-            tma_load_2d(sb, &a.b[r], k * kBK, (j - r * a.tpr) * kBN, &full[slot]);
-          } else if constexpr (MODE == kDW) {
-            const int per = a.nk / a.planes, plane = k / per, kk = k - plane * per;
-#pragma unroll
-            for (int i = 0; i < kBM / 64; ++i)
-              tma_load_3d(sa + i * 8192, &a.a, w.m * kBM + i * 64, kk * kBK, plane, &full[slot]);
-#pragma unroll
-            for (int i = 0; i < kBN / 64; ++i)
-              tma_load_2d(sb + i * 8192, &a.b[0], w.n * kBN + i * 64, kk * kBK, &full[slot]);
+            tma_load_2d(sa, &a.a, k * kBK, am, bar);
+            tma_load_2d(sb, &a.b[r], k * kBK, (j - r * a.tpr) * kBN + (int)c * kHalf, bar);
           } else {
             const int per = a.nk / a.planes, plane = k / per, kk = k - plane * per;
-            const int j = a.j0 + kk * kBK / kBN, r = j / a.tpr;
-            const int row = (j - r * a.tpr) * kBN + kk * kBK % kBN;
-            tma_load_3d(sa, &a.a, kk * kBK, w.m * kBM, plane, &full[slot]);
-#pragma unroll
-            for (int i = 0; i < kBN / 64; ++i)
-              tma_load_2d(sb + i * 8192, &a.b[r], w.n * kBN + i * 64, row, &full[slot]);
+            int row = kk * kBK, r = 0;
+            if constexpr (MODE == kDW) {
+              tma_load_3d(sa, &a.a, am, kk * kBK, plane, bar);
+              tma_load_3d(sa + 8192, &a.a, am + 64, kk * kBK, plane, bar);
+            } else {
+              const int j = a.j0 + kk * kBK / kBN;
+              r = j / a.tpr;
+              row = (j - r * a.tpr) * kBN + kk * kBK % kBN;
+              tma_load_3d(sa, &a.a, kk * kBK, am, plane, bar);
+            }
+            tma_load_2d(sb, &a.b[r], bn, row, bar);
+            tma_load_2d(sb + 8192, &a.b[r], bn + 64, row, bar);
           }
         }
       }
-      if (!ok) {  // wait (bounded) for this block's copies in flight
-        const uint32_t n = it < kStages ? it : kStages;
-        for (uint32_t i = it - n; i < it; ++i)
-          mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1, kWaitLimitNs);
+      // the pair's copies in flight: counted on the first block's barriers, and
+      // the other block stays until the cluster barrier at the end
+      if (!ok && c == 0) {
+        const uint32_t n = it < S ? it : S;
+        for (uint32_t i = it - n; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, kWaitLimitNs);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
+  } else if (warp == kEpiWarps + 1) {
+    if (lane == 0 && c == 0) {
       constexpr uint32_t idesc = tc_idesc(kBM, kBN, A_MN, B_MN);
       constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
       uint32_t it = 0, i = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < a.tiles; t += gridDim.x, ++i) {
+      for (uint32_t t = pair; ok && t < a.tiles; t += pairs) {
         const TileAt w = tile_at(a, t);
         const int k0 = w.s * a.kper, k1 = min(a.nk, k0 + a.kper);
-        const uint32_t acc = i & 1, d = tmem + acc * kBN;
-        if (i >= 2 && !flow.wait(&acc_empty[acc], (i / 2 - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        for (int k = k0; k < k1; ++k, ++it) {
-          const uint32_t slot = it % kStages;
-          if (!flow.wait(&full[slot], (it / kStages) & 1)) {
+        for (int kc = k0; ok && kc < k1; kc += LOGITS ? kChunk : k1 - k0, ++i) {
+          const int ke = LOGITS ? min(k1, kc + kChunk) : k1;
+          const uint32_t acc = i & 1, d = tmem + acc * kBN;
+          if (i >= 2 && !flow.wait(&acc_empty[acc], (i / 2 - 1) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t sa = smem0 + slot * kStageBytes, sb = sa + kABytes;
-          const uint64_t da = tc_desc(sa, A_MN ? 8192 : 16), db = tc_desc(sb, B_MN ? 8192 : 16);
+          for (int k = kc; k < ke; ++k, ++it) {
+            const uint32_t slot = it % S;
+            if (!flow.wait(&full[slot], (it / S) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t sa = smem0 + slot * kStageBytes, sb = sa + kOpBytes;
+            const uint64_t da = tc_desc(sa, A_MN ? 8192 : 16), db = tc_desc(sb, B_MN ? 8192 : 16);
 #pragma unroll
-          for (int q = 0; q < kBK / 16; ++q)
-            tc_mma(d, da + q * a_step, db + q * b_step, idesc, k > k0 || q > 0);
-          tc_commit(&empty[slot]);
+            for (int q = 0; q < kBK / 16; ++q)
+              tc_mma(d, da + q * a_step, db + q * b_step, idesc, k > kc || q > 0);
+            tc_commit(&empty[slot]);
+          }
+          if (ok) tc_commit(&acc_full[acc]);
         }
-        if (ok) tc_commit(&acc_full[acc]);
       }
       if (!ok) {  // the products in flight read shared memory and write tensor memory
         tc_commit(&drained);
@@ -239,51 +286,92 @@ __global__ void __launch_bounds__(kNT, 1) rc_ce_gemm_kernel(const __grid_constan
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
-    const int quad = warp & 3;
-    uint32_t i = 0;
-    for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x, ++i) {
+  } else {
+    const int quad = warp & 3, quarter = warp >> 2;
+    const int row_l = quad * 32 + lane;  // row of the block's half
+    const uint32_t src0 = tmem + quarter * 64 + ((uint32_t)(quad * 32) << 16);
+    const uint32_t box = smem0 + S * kStageBytes + warp * kBoxBytes;
+    const uint32_t acc_empty_addr = first_block_addr(&acc_empty[0]);
+    uint32_t i = 0, nth = 0;
+    bool ok = true;
+    for (uint32_t t = pair; t < a.tiles; t += pairs, ++nth) {
       const TileAt w = tile_at(a, t);
-      const uint32_t acc = i & 1;
-      const int64_t row = (int64_t)w.m * kBM + quad * 32 + lane;  // row of this thread (kDW: column of G)
-      if (!__all_sync(0xffffffffu, flow.wait(&acc_full[acc], (i / 2) & 1))) break;
-      tc_fence_after_sync();
-      const uint32_t src = tmem + acc * kBN + ((uint32_t)(quad * 32) << 16);
-      if constexpr (MODE == kStats || MODE == kGrad) {
+      const int row0 = w.m * kBM + (int)c * kHalf + quad * 32;  // the warp's first row (kDW: column of G)
+      const int row = row0 + lane;
+      float z[64];
+#pragma unroll
+      for (int q = 0; q < 64; ++q) z[q] = 0.0f;
+      // the tile's sum, chunk by chunk
+      const int nc = LOGITS ? (a.nk + kChunk - 1) / kChunk : 1;
+#pragma unroll 1
+      for (int u = 0; u < nc; ++u, ++i) {
+        const uint32_t acc = i & 1;
+        if (!__all_sync(0xffffffffu, flow.wait(&acc_full[acc], (i / 2) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+#pragma unroll
+        for (int q = 0; q < 64; q += 16) {
+          float v[16];
+          tmem_load16(src0 + acc * kBN + q, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[q + e] += v[e];
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_addr + acc * 8);
+      }
+      if (!ok) break;
+      if constexpr (LOGITS) {
         const int j = a.j0 + w.n, r = j / a.tpr, v0 = (j - r * a.tpr) * kBN;
-        const int cols = max(0, min(kBN, a.rows[r] - v0));
+        const int cols = max(0, min(kBN, a.rows[r] - v0)) - quarter * 64;  // of this warp's 64
         const bool live = row < a.N;
         const int y = live ? a.target[row] : 0;
-        const int64_t yt = (int64_t)y - ((int64_t)r * a.C + v0);  // the target's column in this tile, if it is in it
-        const int ycol = (y != a.ignore && yt >= 0 && yt < cols) ? (int)yt : -1;
+        const int yt = y - (r * a.C + v0 + quarter * 64);
+        // the target's column among this warp's, if it is one of them
+        const int ycol = (y != a.ignore && y >= 0 && yt >= 0 && yt < min(cols, 64)) ? yt : -1;
         if constexpr (MODE == kStats) {
-          float m = -INFINITY, s = 0.0f, zt = 0.0f;
-#pragma unroll 1
-          for (int c = 0; c < kBN; c += 32) {
-            float z[32];
-            tmem_load32(src + c, z);
-            if (c + 32 > cols) {
+          if (cols < 64) {
 #pragma unroll
-              for (int q = 0; q < 32; ++q) z[q] = c + q < cols ? z[q] : -INFINITY;
-            }
-            if ((ycol & ~31) == c) {
-#pragma unroll
-              for (int q = 0; q < 32; ++q) zt = (ycol & 31) == q ? z[q] : zt;
-            }
-            float cm = z[0];
-#pragma unroll
-            for (int q = 1; q < 32; ++q) cm = fmaxf(cm, z[q]);
-            const float nm = fmaxf(m, cm);
-            const float base = nm > -INFINITY ? nm * kLog2e : 0.0f;
-            float cs = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 32; ++q) cs += ex2(fmaf(z[q], kLog2e, -base));
-            s = fmaf(s, ex2(fmaf(m, kLog2e, -base)), cs);
-            m = nm;
+            for (int q = 0; q < 64; ++q) z[q] = q < cols ? z[q] : -INFINITY;
           }
-          if (live) {
-            a.part[(int64_t)j * a.N + row] = make_float2(m, s);
-            if (ycol >= 0) a.ztarget[row] = zt;
+          if (ycol >= 0) {
+            float zt = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 64; ++q) zt = ycol == q ? z[q] : zt;
+            a.ztarget[row] = zt;
+          }
+          float m = z[0];
+#pragma unroll
+          for (int q = 1; q < 64; ++q) m = fmaxf(m, z[q]);
+          const float base = m > -INFINITY ? m * kLog2e : 0.0f;
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 64; q += 2) {
+            s0 += ex2(fmaf(z[q], kLog2e, -base));
+            s1 += ex2(fmaf(z[q + 1], kLog2e, -base));
+          }
+          // the four warps of these rows; the first one writes the tile's pair
+          if (quarter != 0 && nth > 0 &&
+              !__all_sync(0xffffffffu, flow.wait(&join_free[quad], (nth - 1) & 1)))
+            break;
+          join[quarter][row_l] = make_float2(m, s0 + s1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&joined[quad]);
+          if (quarter == 0) {
+            if (!__all_sync(0xffffffffu, flow.wait(&joined[quad], nth & 1))) break;
+            float2 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = join[q][row_l];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&join_free[quad]);
+            const float nm = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+            const float nb = nm > -INFINITY ? nm * kLog2e : 0.0f;
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s = fmaf(v[q].y, ex2(fmaf(v[q].x, kLog2e, -nb)), s);
+            if (live) a.part[(size_t)j * a.N + row] = make_float2(nm, s);
           }
         } else {
           const float lse2 = live ? a.lse_in[row] * kLog2e : 0.0f;
@@ -291,99 +379,106 @@ __global__ void __launch_bounds__(kNT, 1) rc_ce_gemm_kernel(const __grid_constan
           // a label that is no word and not the ignored one poisons its row
           if (y < 0 || y >= a.V) g = __int_as_float(0x7fc00000);
           const bool zero = !live || y == a.ignore;
-          char *out = a.g + ((int64_t)row * a.gcols + (int64_t)w.n * kBN) * 2;
-          const int64_t plane = a.N * (int64_t)a.gcols * 2;
-#pragma unroll 1
-          for (int c = 0; c < kBN; c += 32) {
-            float z[32];
-            tmem_load32(src + c, z);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              float pr = ex2(fmaf(z[q], kLog2e, -lse2));
-              pr -= c + q == ycol ? 1.0f : 0.0f;
-              z[q] = (zero || c + q >= cols) ? 0.0f : pr * g;
-            }
-            if (live) {
+          for (int q = 0; q < 64; ++q) {
+            float pr = ex2(fmaf(z[q], kLog2e, -lse2));
+            pr -= q == ycol ? 1.0f : 0.0f;
+            z[q] = (zero || q >= cols) ? 0.0f : pr * g;
+          }
+          for (int plane = 0; plane < a.planes; ++plane) {
+            staging_free(lane);
 #pragma unroll
-              for (int q = 0; q < 32; q += 8) {
-                uint32_t hi[4];
+            for (int q = 0; q < 64; q += 8) {
+              uint32_t h[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) hi[u] = pack_bf16x2(z[q + 2 * u], z[q + 2 * u + 1]);
-                st_v4(out + (c + q) * 2, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                if (a.planes == 2) {
-                  uint32_t lo[4];
-#pragma unroll
-                  for (int u = 0; u < 4; ++u)
-                    lo[u] = pack_bf16x2(z[q + 2 * u] - __uint_as_float(hi[u] << 16),
-                                        z[q + 2 * u + 1] - __uint_as_float(hi[u] & 0xffff0000u));
-                  st_v4(out + plane + (c + q) * 2, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                }
+              for (int e = 0; e < 4; ++e) {
+                h[e] = pack_bf16x2(z[q + 2 * e], z[q + 2 * e + 1]);
+                z[q + 2 * e] -= __uint_as_float(h[e] << 16);  // what the next plane holds
+                z[q + 2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
               }
+              sts128(staging_unit(box, lane, q / 8), make_uint4(h[0], h[1], h[2], h[3]));
+            }
+            staging_ready();
+            if (lane == 0 && row0 < a.N) {
+              tma_store_3d(&a.out[0], w.n * kBN + quarter * 64, row0, plane, box);
+              bulk_commit();
             }
           }
         }
       } else if constexpr (MODE == kDW) {
-        const int j = a.j0 + w.m / 2, r = j / a.tpr;
-        const int v = (j - r * a.tpr) * kBN + (w.m & 1) * kBM + quad * 32 + lane;
-        const bool live = v < a.rows[r];
-        char *out = a.dw[r] + ((int64_t)v * a.D + (int64_t)w.n * kBN) * 2;
-        const int cols = min(kBN, a.D - w.n * kBN);
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
-          float z[32];
-          tmem_load32(src + c, z);
-          if (!live) continue;
-          if (a.dw_vec) {
+        const int j = a.j0 + w.m, r = j / a.tpr;
+        const int v0 = (j - r * a.tpr) * kBN + (int)c * kHalf + quad * 32;  // the warp's first row of W_r
+        const int x0 = w.n * kBN + quarter * 64;
+        if (a.dw_tma) {
+          staging_free(lane);
 #pragma unroll
-            for (int q = 0; q < 32; q += 8)
-              if (c + q < cols)
-                st_v4(out + (c + q) * 2, make_uint4(pack_bf16x2(z[q], z[q + 1]), pack_bf16x2(z[q + 2], z[q + 3]),
-                                                    pack_bf16x2(z[q + 4], z[q + 5]), pack_bf16x2(z[q + 6], z[q + 7])));
-          } else {
-#pragma unroll
-            for (int q = 0; q < 32; ++q)
-              if (c + q < cols) store_elem<BF16>(out, c + q, z[q]);
+          for (int q = 0; q < 64; q += 8)
+            sts128(staging_unit(box, lane, q / 8),
+                   make_uint4(pack_bf16x2(z[q], z[q + 1]), pack_bf16x2(z[q + 2], z[q + 3]),
+                              pack_bf16x2(z[q + 4], z[q + 5]), pack_bf16x2(z[q + 6], z[q + 7])));
+          staging_ready();
+          if (lane == 0 && v0 < a.rows[r] && x0 < a.D) {
+            tma_store_2d(&a.out[r], x0, v0, box);
+            bulk_commit();
           }
+        } else {
+          // through the staging rows too, so that a warp's stores are neighbours
+          staging_free(lane);
+#pragma unroll
+          for (int q = 0; q < 64; q += 8)
+            sts128(staging_unit(box, lane, q / 8),
+                   make_uint4(pack_bf16x2(z[q], z[q + 1]), pack_bf16x2(z[q + 2], z[q + 3]),
+                              pack_bf16x2(z[q + 4], z[q + 5]), pack_bf16x2(z[q + 6], z[q + 7])));
+          __syncwarp();
+          const int n = min(32, a.rows[r] - v0);
+          for (int e = 0; e < n; ++e) {
+            uint16_t *out = reinterpret_cast<uint16_t *>(a.dw[r]) + (int64_t)(v0 + e) * a.D;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int x = h * 32 + lane;
+              uint16_t v;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(staging_unit(box, e, x / 8) + (x & 7) * 2));
+              if (x0 + x < a.D) out[x0 + x] = v;
+            }
+          }
+          __syncwarp();
         }
       } else {
-        const bool live = row < a.N;
-        float *out = a.dh + ((int64_t)w.s * a.N + row) * a.dpad + (int64_t)w.n * kBN;
-        const int cols = min(kBN, a.dpad - w.n * kBN);  // a multiple of 8
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
-          float z[32];
-          tmem_load32(src + c, z);
-          if (!live) continue;
+        const int x0 = w.n * kBN + quarter * 64;
 #pragma unroll
-          for (int q = 0; q < 32; q += 4) {
-            if (c + q < cols) {
-              float4 *o = reinterpret_cast<float4 *>(out + c + q);
-              float4 v = make_float4(z[q], z[q + 1], z[q + 2], z[q + 3]);
-              if (!a.first) {
-                const float4 u = *o;
-                v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-              }
-              *o = v;
-            }
+        for (int h = 0; h < 2; ++h) {
+          staging_free(lane);
+#pragma unroll
+          for (int q = 0; q < 32; q += 4)
+            sts128(staging_unit(box, lane, q / 4),
+                   make_uint4(__float_as_uint(z[h * 32 + q]), __float_as_uint(z[h * 32 + q + 1]),
+                              __float_as_uint(z[h * 32 + q + 2]), __float_as_uint(z[h * 32 + q + 3])));
+          staging_ready();
+          // one add per element and launch, launches in stream order: a fixed order
+          if (lane == 0 && row0 < a.N && x0 + h * 32 < a.D) {
+            if (a.first) tma_store_3d(&a.out[0], x0 + h * 32, row0, w.s, box);
+            else tma_add_3d(&a.out[0], x0 + h * 32, row0, w.s, box);
+            bulk_commit();
           }
         }
       }
-      tc_fence_before_sync();
-      mbar_arrive(&acc_empty[acc]);
     }
+    if (MODE != kStats && lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   __syncthreads();
-  if (warp == 2) tmem_free_all(tmem);
+  cluster_sync();  // the other block's copies and products no longer touch this one
+  if (warp == kEpiWarps + 1) tmem_free_all(tmem);
 }
 
 // Joins the tiles' (max, sum) pairs of each row in a fixed order:
 // a block has 2^lg rows and 256 / 2^lg threads per row.
-__global__ void __launch_bounds__(kNT) rc_ce_join_kernel(const float2 *part, const float *ztarget,
+__global__ void __launch_bounds__(kThreads) rc_ce_join_kernel(const float2 *part, const float *ztarget,
                                                          const int32_t *target, float *loss, float *lse, int64_t N,
                                                          int64_t V, int tiles, int lg, int ignore) {
-  __shared__ float sm[kNT], ss[kNT];
+  __shared__ float sm[kThreads], ss[kThreads];
   pdl_wait();
-  const int rx = threadIdx.x & ((1 << lg) - 1), ty = threadIdx.x >> lg, nty = kNT >> lg;
+  const int rx = threadIdx.x & ((1 << lg) - 1), ty = threadIdx.x >> lg, nty = kThreads >> lg;
   const int64_t row = ((int64_t)blockIdx.x << lg) + rx;
   float m = -INFINITY, s = 0.0f;
   if (row < N) {
@@ -420,12 +515,12 @@ __global__ void __launch_bounds__(kNT) rc_ce_join_kernel(const float2 *part, con
 // dst[row][0, dpad) = src[row][0, D), zero behind D, and zero in rows whose
 // target is ignored (target NULL: none), so that whatever a padded row holds
 // stays out of the products.
-__global__ void __launch_bounds__(kNT) rc_ce_pack_kernel(const uint16_t *src, uint16_t *dst, const int32_t *target,
+__global__ void __launch_bounds__(kThreads) rc_ce_pack_kernel(const uint16_t *src, uint16_t *dst, const int32_t *target,
                                                          int64_t rows, int D, int dpad, int ignore) {
   pdl_wait();
   const int per = dpad / 8;
   const int64_t n = rows * per;
-  for (int64_t u = (int64_t)blockIdx.x * kNT + threadIdx.x; u < n; u += (int64_t)gridDim.x * kNT) {
+  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (int64_t)gridDim.x * kThreads) {
     const int64_t row = u / per;
     const int c = (int)(u - row * per) * 8;
     const bool skip = target != nullptr && target[row] == ignore;
@@ -441,17 +536,32 @@ __global__ void __launch_bounds__(kNT) rc_ce_pack_kernel(const uint16_t *src, ui
   }
 }
 
-// dh = bf16(sum of the splits' sums, in order).
-__global__ void __launch_bounds__(kNT) rc_ce_finish_kernel(const float *sums, char *dh, int64_t N, int D, int dpad,
-                                                           int splits) {
+// dh = bf16(sum of the splits' sums, in order).  A thread has 8 columns of a
+// row (dpad is a multiple of 8); `vec`: dh's rows are 16-byte multiples.
+__global__ void __launch_bounds__(kThreads) rc_ce_finish_kernel(const float *sums, char *dh, int64_t N, int D, int dpad,
+                                                                int splits, bool vec) {
   pdl_wait();
-  const int64_t n = N * D;
-  for (int64_t u = (int64_t)blockIdx.x * kNT + threadIdx.x; u < n; u += (int64_t)gridDim.x * kNT) {
-    const int64_t row = u / D;
-    const float *at = sums + row * dpad + (u - row * D);
-    float v = at[0];
-    for (int s = 1; s < splits; ++s) v += at[(int64_t)s * N * dpad];
-    store_elem<BF16>(dh, u, v);
+  const int per = dpad / 8;
+  const int64_t n = N * per;
+  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = u / per;
+    const int x = (int)(u - row * per) * 8;
+    float v[8];
+    for (int s = 0; s < splits; ++s) {
+      const char *at = reinterpret_cast<const char *>(sums + ((int64_t)s * N + row) * dpad + x);
+      float p[8];
+      unpack<F32>(ld_stream_v4(at), *reinterpret_cast<float(*)[4]>(p));
+      unpack<F32>(ld_stream_v4(at + 16), *reinterpret_cast<float(*)[4]>(p + 4));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = s == 0 ? p[e] : v[e] + p[e];
+    }
+    if (vec) {
+      store_vec<BF16, 8>(dh + (row * D + x) * 2, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (x + e < D) store_elem<BF16>(dh, row * D + x + e, v[e]);
+    }
   }
 }
 
@@ -471,20 +581,21 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// A bf16 matrix [planes][rows][cols], `pitch` elements from row to row, read
-// in boxes of 64 columns x box_rows rows with the 128-byte swizzle; what lies
-// outside reads as zero.
+// A matrix [planes][rows][cols] (planes 0: a plain one), `pitch` elements from
+// row to row, moved in boxes of 128 bytes x box_rows rows with the 128-byte
+// swizzle; what lies outside reads as zero and is not written.
 bool make_map(CUtensorMap *map, const void *base, int64_t planes, int64_t rows, int64_t cols, int64_t pitch,
-              int box_rows) {
+              int box_rows, bool f32 = false) {
   EncodeFn fn = encode_fn();
   if (!fn) return false;
-  const int rank = planes > 0 ? 3 : 2;
+  const int rank = planes > 0 ? 3 : 2, esz = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)std::max<int64_t>(planes, 1)};
-  const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch * esz, (cuuint64_t)pitch * esz * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)box_rows, 1};
   const cuuint32_t es[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+            const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -520,9 +631,9 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
     q.off_part = take((size_t)q.tiles * N * 8);
     q.off_zt = take(N * 4);
   } else {
-    // two planes up to 128 tokens: one row tile, whose products take less
-    // time than reading the weights even when there are twice as many
-    q.planes = s.tokens <= kBM ? 2 : 1;
+    // two planes up to 128 tokens: the products take less time than reading the
+    // weights even when there are twice as many
+    q.planes = s.tokens <= 128 ? 2 : 1;
     const int64_t tile_bytes = (int64_t)q.planes * s.tokens * kBN * 2;
     const int64_t want = std::max<int64_t>(16, (64ll << 20) / tile_bytes);
     q.pieces = (int)cdiv(q.tiles, std::min<int64_t>(want, q.tiles));
@@ -531,7 +642,7 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
     // few output tiles of dh: split its long k (the piece's columns)
     const int64_t nk = (int64_t)q.planes * q.per_piece * (kBN / kBK);
     const int64_t out_tiles = cdiv(s.tokens, kBM) * cdiv(s.d, kBN);
-    int64_t sp = std::max<int64_t>(1, std::min<int64_t>(device_sm_count() / out_tiles, nk / 8));
+    int64_t sp = std::max<int64_t>(1, std::min<int64_t>(device_sm_count() / 2 / out_tiles, nk / 8));
     q.kper = (int)cdiv(nk, sp);
     q.splits = (int)cdiv(nk, q.kper);
     q.off_g = take((size_t)q.planes * N * q.per_piece * kBN * 2);
@@ -543,23 +654,32 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
 
 template <int MODE>
 cudaError_t gemm(CeParams &a, cudaStream_t s) {
-  cudaError_t err = cudaFuncSetAttribute(rc_ce_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemBytes);
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    err = cudaFuncSetAttribute(rc_ce_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)smem_bytes(MODE));
+    if (err != cudaSuccess) return err;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   if (a.splits < 1) {
     a.splits = 1;
     a.kper = a.nk;
   }
-  a.tiles = (int64_t)a.mt * a.nt * a.splits;
-  const int64_t grid = std::min<int64_t>(a.tiles, device_sm_count());
-  return launch_kernel(rc_ce_gemm_kernel<MODE>, dim3((unsigned)grid), dim3(kNT), kSmemBytes, s, a);
+  const int64_t tiles = (int64_t)a.mt * a.nt * a.splits;
+  if (tiles > 0x40000000) return cudaErrorInvalidValue;  // (beyond what fits in memory)
+  a.tiles = (uint32_t)tiles;
+  const int64_t pairs = std::min<int64_t>(tiles, device_sm_count() / 2);
+  return launch_kernel(rc_ce_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs)), dim3(kNT), smem_bytes(MODE), s, a);
 }
 
 cudaError_t pack(const void *src, void *dst, const int32_t *target, int64_t rows, int D, int dpad, int ignore,
                  cudaStream_t s) {
   const int64_t n = rows * (dpad / 8);
-  const int64_t grid = std::min<int64_t>(cdiv(n, kNT), (int64_t)device_sm_count() * 8);
-  return launch_kernel(rc_ce_pack_kernel, dim3((unsigned)grid), dim3(kNT), 0, s,
+  const int64_t grid = std::min<int64_t>(cdiv(n, kThreads), (int64_t)device_sm_count() * 8);
+  return launch_kernel(rc_ce_pack_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
                        static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), target, rows, D, dpad,
                        ignore);
 }
@@ -617,13 +737,13 @@ cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s) {
   if ((err = operands(j, q, copies, &o, a.rows, s)) != cudaSuccess) return err;
   const int D = j.shape.d;
   const int64_t N = j.shape.tokens;
-  if (!make_map(&a.a, o.h, 0, N, D, o.pitch, kBM)) return cudaErrorInvalidValue;
+  if (!make_map(&a.a, o.h, 0, N, D, o.pitch, kHalf)) return cudaErrorInvalidValue;
   for (int r = 0; r < q.ranks; ++r)
-    if (!make_map(&a.b[r], o.w[r], 0, a.rows[r], D, o.pitch, kBN)) return cudaErrorInvalidValue;
+    if (!make_map(&a.b[r], o.w[r], 0, a.rows[r], D, o.pitch, kHalf)) return cudaErrorInvalidValue;
   a.target = j.target;
   a.part = reinterpret_cast<float2 *>(ws + q.off_part);
   a.ztarget = reinterpret_cast<float *>(ws + q.off_zt);
-  a.N = N;
+  a.N = (int)N;
   a.D = D;
   a.C = q.C;
   a.tpr = q.tpr;
@@ -634,8 +754,8 @@ cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s) {
   if ((err = gemm<kStats>(a, s)) != cudaSuccess) return err;
   // as many rows per block as leave every thread of a row a tile or more
   int lg = 5;
-  while (lg > 0 && ((kNT >> lg) < q.tiles && (1 << (lg - 1)) >= N)) --lg;
-  return launch_kernel(rc_ce_join_kernel, dim3((unsigned)cdiv(N, 1 << lg)), dim3(kNT), 0, s,
+  while (lg > 0 && ((kThreads >> lg) < q.tiles && (1 << (lg - 1)) >= N)) --lg;
+  return launch_kernel(rc_ce_join_kernel, dim3((unsigned)cdiv(N, 1 << lg)), dim3(kThreads), 0, s,
                        (const float2 *)a.part, (const float *)a.ztarget, j.target, j.loss, j.lse, N,
                        (int64_t)j.shape.vocab, q.tiles, lg, j.ignore);
 }
@@ -653,39 +773,39 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
   base.target = j.target;
   base.lse_in = j.lse_in;
   base.dloss = j.dloss;
-  base.g = ws + q.off_g;
-  base.dh = reinterpret_cast<float *>(ws + q.off_dh);
-  base.N = N;
+  char *const g = ws + q.off_g;
+  float *const sums = reinterpret_cast<float *>(ws + q.off_dh);
+  base.N = (int)N;
   base.D = D;
-  base.dpad = q.dpad;
   base.C = q.C;
   base.tpr = q.tpr;
   base.planes = q.planes;
   base.ignore = j.ignore;
-  base.V = j.shape.vocab;
-  base.dw_vec = D % 8 == 0;
+  base.V = (int)j.shape.vocab;
+  base.dw_tma = D % 8 == 0;
   for (int r = 0; r < q.ranks; ++r) {
     base.dw[r] = static_cast<char *>(j.dweight[r]);
-    base.dw_vec = base.dw_vec && reinterpret_cast<uintptr_t>(j.dweight[r]) % 16 == 0;
+    base.dw_tma = base.dw_tma && reinterpret_cast<uintptr_t>(j.dweight[r]) % 16 == 0;
   }
   CeParams z = base, w = base, h = base;
-  if (!make_map(&z.a, o.h, 0, N, D, q.dpad, kBM) || !make_map(&w.b[0], o.h, 0, N, D, q.dpad, 64))
-    return cudaErrorInvalidValue;
-  for (int r = 0; r < q.ranks; ++r)
-    if (!make_map(&z.b[r], o.w[r], 0, base.rows[r], D, o.pitch, kBN) ||
-        !make_map(&h.b[r], o.w[r], 0, base.rows[r], D, o.pitch, 64))
-      return cudaErrorInvalidValue;
-  for (int i = 0; i < q.pieces; ++i) {
+  bool ok = make_map(&z.a, o.h, 0, N, D, q.dpad, kHalf) && make_map(&w.b[0], o.h, 0, N, D, q.dpad, 64) &&
+            make_map(&h.out[0], sums, q.splits, N, D, q.dpad, 32, true);
+  for (int r = 0; r < q.ranks; ++r) {
+    ok = ok && make_map(&z.b[r], o.w[r], 0, base.rows[r], D, o.pitch, kHalf) &&
+         make_map(&h.b[r], o.w[r], 0, base.rows[r], D, o.pitch, 64);
+    if (base.dw_tma) ok = ok && make_map(&w.out[r], base.dw[r], 0, base.rows[r], D, D, 32);
+  }
+  for (int i = 0; ok && i < q.pieces; ++i) {
     const int j0 = i * q.per_piece, nt = std::min(q.per_piece, q.tiles - j0), cols = nt * kBN;
     z.j0 = w.j0 = h.j0 = j0;
-    z.gcols = w.gcols = h.gcols = cols;
-    if (!make_map(&w.a, base.g, q.planes, N, cols, cols, 64) || !make_map(&h.a, base.g, q.planes, N, cols, cols, kBM))
-      return cudaErrorInvalidValue;
+    ok = make_map(&z.out[0], g, q.planes, N, cols, cols, 32) && make_map(&w.a, g, q.planes, N, cols, cols, 64) &&
+         make_map(&h.a, g, q.planes, N, cols, cols, kHalf);
+    if (!ok) break;
     z.mt = (int)cdiv(N, kBM);
     z.nt = nt;
     z.nk = (int)cdiv(D, kBK);
     if ((err = gemm<kGrad>(z, s)) != cudaSuccess) return err;
-    w.mt = cols / kBM;
+    w.mt = nt;
     w.nt = (int)cdiv(D, kBN);
     w.nk = q.planes * (int)cdiv(N, kBK);
     if ((err = gemm<kDW>(w, s)) != cudaSuccess) return err;
@@ -697,9 +817,11 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
     h.first = i == 0;
     if ((err = gemm<kDH>(h, s)) != cudaSuccess) return err;
   }
-  const int64_t grid = std::min<int64_t>(cdiv(N * D, kNT), (int64_t)device_sm_count() * 8);
-  return launch_kernel(rc_ce_finish_kernel, dim3((unsigned)grid), dim3(kNT), 0, s, (const float *)base.dh,
-                       static_cast<char *>(j.dhidden), N, D, q.dpad, q.splits);
+  if (!ok) return cudaErrorInvalidValue;
+  const int64_t grid = std::min<int64_t>(cdiv(N * (q.dpad / 8), kThreads), (int64_t)device_sm_count() * 8);
+  const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(j.dhidden) % 16 == 0;
+  return launch_kernel(rc_ce_finish_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, (const float *)sums,
+                       static_cast<char *>(j.dhidden), N, D, q.dpad, q.splits, vec);
 }
 
 cudaError_t read_and_clear_ce_timeouts(unsigned int *count) {
