@@ -53,13 +53,16 @@ constexpr int kBK = 64;        // one 128-byte row of bf16
 constexpr uint32_t kOpBytes = kHalf * kBK * 2;       // 16 KiB of either operand per block and stage
 constexpr uint32_t kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kBoxBytes = 4096;                 // an epilogue warp's staging: 32 rows of 128 bytes
-constexpr int kGroupM = 8;     // row tiles that share a sweep over the columns (L2 reuse)
+constexpr int kGroupM = 16;    // row tiles that share a sweep over the columns (L2 reuse; 8: 2% slower at 8192 rows, 4: 7%)
 // The tensor cores add to their fp32 accumulators by truncation, which pulls
-// a long sum towards zero by about 2^-24 per step.  The logits are therefore
-// summed in chunks of 512 products; the chunks are added in registers with
-// ordinary rounding.  (4096-wide, 2048 tokens: the loss is 4e-7 off its 64-bit
-// value instead of 2.2e-6.)
-constexpr int kChunk = 8;      // steps of k per chunk
+// a long sum towards zero by about 2^-24 per step.  Where the logits' own
+// error is what the caller sees (the loss, and G in two planes) they are
+// summed in chunks of 1024 products, and the chunks are added in registers
+// with ordinary rounding.  Relative error of the loss at d = 4096 in chunks of
+// 512, 1024, 2048 products and in one: 2.4e-7, 5.1e-7, 1.1e-6, 2.2e-6 (32-bit
+// products on the CUDA cores: 4.4e-7); each chunk costs about 600 cycles of
+// tensor time to a tile's 512 per 64 products.
+constexpr int kChunk = 16;     // steps of k per chunk
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 256;  // of the small kernels
@@ -93,6 +96,7 @@ struct alignas(64) CeParams {
   int j0;                     // first tile of this launch's piece
   int planes;                 // bf16 planes of G
   int mt, nt, nk, kper, splits;
+  int chunk;                  // kStats, kGrad: steps of k that one accumulator sums
   uint32_t tiles;
   int ignore;
   bool first;                 // kDH: store instead of add
@@ -155,6 +159,16 @@ __device__ __forceinline__ uint32_t staging_unit(uint32_t box, int lane, int u) 
   return box + lane * 128 + ((u ^ (lane & 7)) << 4);
 }
 
+// kDH: where step kk of the piece's columns lies in the ranks' rows, and how
+// many steps are left in that rank's piece.
+__device__ __forceinline__ void dh_row(const CeParams &a, int kk, int *r, int *row, int *left) {
+  const int per = a.tpr * (kBN / kBK), at = a.j0 * (kBN / kBK) + kk;
+  *r = at / per;
+  const int in = at - *r * per;
+  *row = in * kBK;
+  *left = per - in;
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     rc_ce_gemm_kernel(const __grid_constant__ CeParams a) {
@@ -201,41 +215,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
 
   if (warp == kEpiWarps) {
     if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
+      uint32_t it = 0, slot = 0, phase = 0;
+      bool ok = true, full_round = false;  // full_round: every slot has been filled once
+      const uint32_t full0 = first_block_addr(&full[0]);
+      const int per_plane = LOGITS ? 0 : a.nk / a.planes;
       for (uint32_t t = pair; ok && t < a.tiles; t += pairs) {
         const TileAt w = tile_at(a, t);
         const int k0 = w.s * a.kper, k1 = min(a.nk, k0 + a.kper);
-        for (int k = k0; k < k1; ++k, ++it) {
-          const uint32_t slot = it % S;
-          if (it >= S && !flow.wait(&empty[slot], (it / S - 1) & 1)) {
+        const int am = w.m * kBM + (int)c * kHalf, bn = w.n * kBN + (int)c * kHalf;
+        // what a step needs is carried from step to step: this thread has a few
+        // hundred cycles for each, and a division would take most of them
+        const CUtensorMap *bmap = &a.b[0];
+        int plane = 0, kk = k0, row = 0, left = 0, r = 0;
+        if constexpr (LOGITS) {
+          const int j = a.j0 + w.n;
+          r = j / a.tpr;
+          bmap = &a.b[r];
+          row = (j - r * a.tpr) * kBN + (int)c * kHalf;
+        } else {
+          plane = k0 / per_plane;
+          kk = k0 - plane * per_plane;
+          if constexpr (MODE == kDH) dh_row(a, kk, &r, &row, &left);
+        }
+        for (int k = k0; k < k1; ++k) {
+          if (full_round && !flow.wait(&empty[slot], phase ^ 1)) {
             ok = false;
             break;
           }
           const uint32_t sa = smem0 + slot * kStageBytes, sb = sa + kOpBytes;
           // both blocks' bytes are counted on the first block's barrier
           if (c == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStageBytes);
-          const uint32_t bar = first_block_addr(&full[slot]);
-          const int am = w.m * kBM + (int)c * kHalf, bn = w.n * kBN + (int)c * kHalf;
+          const uint32_t bar = full0 + slot * 8;
           if constexpr (LOGITS) {
-            const int j = a.j0 + w.n, r = j / a.tpr;
             tma_load_2d(sa, &a.a, k * kBK, am, bar);
-            tma_load_2d(sb, &a.b[r], k * kBK, (j - r * a.tpr) * kBN + (int)c * kHalf, bar);
+            tma_load_2d(sb, bmap, k * kBK, row, bar);
           } else {
-            const int per = a.nk / a.planes, plane = k / per, kk = k - plane * per;
-            int row = kk * kBK, r = 0;
             if constexpr (MODE == kDW) {
-              tma_load_3d(sa, &a.a, am, kk * kBK, plane, bar);
-              tma_load_3d(sa + 8192, &a.a, am + 64, kk * kBK, plane, bar);
+              row = kk * kBK;
+              tma_load_3d(sa, &a.a, am, row, plane, bar);
+              tma_load_3d(sa + 8192, &a.a, am + 64, row, plane, bar);
             } else {
-              const int j = a.j0 + kk * kBK / kBN;
-              r = j / a.tpr;
-              row = (j - r * a.tpr) * kBN + kk * kBK % kBN;
+              bmap = &a.b[r];
               tma_load_3d(sa, &a.a, kk * kBK, am, plane, bar);
             }
-            tma_load_2d(sb, &a.b[r], bn, row, bar);
-            tma_load_2d(sb + 8192, &a.b[r], bn + 64, row, bar);
+            tma_load_2d(sb, bmap, bn, row, bar);
+            tma_load_2d(sb + 8192, bmap, bn + 64, row, bar);
+            ++kk;
+            if constexpr (MODE == kDH) {
+              row += kBK;
+              if (--left == 0) {  // the next rank's piece
+                ++r;
+                row = 0;
+                left = a.tpr * (kBN / kBK);
+              }
+            }
+            if (kk == per_plane) {
+              kk = 0;
+              ++plane;
+              if constexpr (MODE == kDH) dh_row(a, 0, &r, &row, &left);
+            }
           }
+          if (++slot == S) {
+            slot = 0;
+            phase ^= 1;
+            full_round = true;
+          }
+          ++it;
         }
       }
       // the pair's copies in flight: counted on the first block's barriers, and
@@ -250,22 +295,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     if (lane == 0 && c == 0) {
       constexpr uint32_t idesc = tc_idesc(kBM, kBN, A_MN, B_MN);
       constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
-      uint32_t it = 0, i = 0;
+      uint32_t slot = 0, phase = 0, i = 0;
       bool ok = true;
       for (uint32_t t = pair; ok && t < a.tiles; t += pairs) {
         const TileAt w = tile_at(a, t);
         const int k0 = w.s * a.kper, k1 = min(a.nk, k0 + a.kper);
-        for (int kc = k0; ok && kc < k1; kc += LOGITS ? kChunk : k1 - k0, ++i) {
-          const int ke = LOGITS ? min(k1, kc + kChunk) : k1;
+        for (int kc = k0; ok && kc < k1; kc += LOGITS ? a.chunk : k1 - k0, ++i) {
+          const int ke = LOGITS ? min(k1, kc + a.chunk) : k1;
           const uint32_t acc = i & 1, d = tmem + acc * kBN;
           if (i >= 2 && !flow.wait(&acc_empty[acc], (i / 2 - 1) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          for (int k = kc; k < ke; ++k, ++it) {
-            const uint32_t slot = it % S;
-            if (!flow.wait(&full[slot], (it / S) & 1)) {
+          for (int k = kc; k < ke; ++k) {
+            if (!flow.wait(&full[slot], phase)) {
               ok = false;
               break;
             }
@@ -276,6 +320,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             for (int q = 0; q < kBK / 16; ++q)
               tc_mma(d, da + q * a_step, db + q * b_step, idesc, k > kc || q > 0);
             tc_commit(&empty[slot]);
+            if (++slot == S) {
+              slot = 0;
+              phase ^= 1;
+            }
           }
           if (ok) tc_commit(&acc_full[acc]);
         }
@@ -302,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
 #pragma unroll
       for (int q = 0; q < 64; ++q) z[q] = 0.0f;
       // the tile's sum, chunk by chunk
-      const int nc = LOGITS ? (a.nk + kChunk - 1) / kChunk : 1;
+      const int nc = LOGITS ? (a.nk + a.chunk - 1) / a.chunk : 1;
 #pragma unroll 1
       for (int u = 0; u < nc; ++u, ++i) {
         const uint32_t acc = i & 1;
@@ -514,25 +562,199 @@ __global__ void __launch_bounds__(kThreads) rc_ce_join_kernel(const float2 *part
 
 // dst[row][0, dpad) = src[row][0, D), zero behind D, and zero in rows whose
 // target is ignored (target NULL: none), so that whatever a padded row holds
-// stays out of the products.
+// stays out of the products.  VEC: src's rows are 16-byte multiples.
+template <bool VEC>
 __global__ void __launch_bounds__(kThreads) rc_ce_pack_kernel(const uint16_t *src, uint16_t *dst, const int32_t *target,
-                                                         int64_t rows, int D, int dpad, int ignore) {
+                                                              int rows, int D, int dpad, int ignore) {
   pdl_wait();
-  const int per = dpad / 8;
-  const int64_t n = rows * per;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = u / per;
-    const int c = (int)(u - row * per) * 8;
+  const uint32_t per = dpad / 8;
+  const uint64_t n = (uint64_t)rows * per;
+  for (uint64_t u = (uint64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (uint64_t)gridDim.x * kThreads) {
+    const uint32_t row = n >> 32 ? (uint32_t)(u / per) : (uint32_t)u / per;
+    const int c = (int)(u - (uint64_t)row * per) * 8;
     const bool skip = target != nullptr && target[row] == ignore;
-    uint32_t w[4];
+    const uint16_t *at = src + (size_t)row * D;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if constexpr (VEC) {
+      if (!skip) v = ld_stream_v4(at + c);
+    } else {
+      uint32_t w[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int x = c + 2 * q;
-      const uint32_t lo = !skip && x < D ? src[row * D + x] : 0u;
-      const uint32_t hi = !skip && x + 1 < D ? src[row * D + x + 1] : 0u;
-      w[q] = lo | (hi << 16);
+      for (int q = 0; q < 4; ++q) {
+        const int x = c + 2 * q;
+        const uint32_t lo = !skip && x < D ? at[x] : 0u;
+        const uint32_t hi = !skip && x + 1 < D ? at[x + 1] : 0u;
+        w[q] = lo | (hi << 16);
+      }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    st_v4(dst + row * dpad + c, make_uint4(w[0], w[1], w[2], w[3]));
+    st_v4(dst + (size_t)row * dpad + c, v);
+  }
+}
+
+// ---------------------------------------------------------------- few tokens
+// The forward pass of up to kFewTokens tokens reads the weights once and does
+// little with them, so it is bound by that read; tensor-core tiles of 256 rows
+// would be nearly empty and take longer than the read.  A warp takes four rows
+// of W at a time, every lane 8 columns of each: 4 loads of 16 bytes (the next
+// 256 columns' four in flight meanwhile), 8 fp32 products per row and token in
+// pairs (fma.rn.f32x2).  The tokens' hidden rows lie in shared memory as bf16.
+// The four rows' sums of all tokens are reduced over the lanes in one
+// butterfly that leaves each (row, token) in a lane of its own, which keeps
+// the token's running maximum and sum of exponentials over the rows it sees.
+constexpr int kFewTokens = 8;
+constexpr uint32_t kFewSmem = 96 * 1024;  // two blocks per SM
+
+struct FewParams {
+  const char *w[kMaxRanks];
+  int rows[kMaxRanks];
+  const char *h;
+  const int32_t *target;
+  float2 *part;     // [block][N]
+  float *ztarget;   // [N]
+  int N, D, dpad, C;
+  uint32_t groups_per_rank, groups;  // groups of four rows
+  int ignore;
+};
+
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  uint64_t r, ua, ub, uc;
+  asm("mov.b64 %0, {%1,%2};" : "=l"(ua) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1,%2};" : "=l"(ub) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1,%2};" : "=l"(uc) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(ua), "l"(ub), "l"(uc));
+  asm("mov.b64 {%0,%1}, %2;" : "=f"(c.x), "=f"(c.y) : "l"(r));
+  return c;
+}
+__device__ __forceinline__ F2 pair_of(uint32_t bf16x2) {
+  return F2{__uint_as_float(bf16x2 << 16), __uint_as_float(bf16x2 & 0xffff0000u)};
+}
+
+// T: tokens, padded to a power of two.  VEC: rows of W are 16-byte multiples.
+template <int T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) rc_ce_few_kernel(const __grid_constant__ FewParams a) {
+  constexpr int R = 4, K = R * T;
+  constexpr int kLog = K == 4 ? 2 : K == 8 ? 3 : K == 16 ? 4 : 5;
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint16_t hs[];  // [T][dpad]
+  __shared__ float2 wpart[kWarps][T];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  const uint16_t *h = reinterpret_cast<const uint16_t *>(a.h);
+  for (int t = 0; t < T; ++t)
+    for (int x = threadIdx.x; x < a.dpad; x += kThreads)
+      hs[t * a.dpad + x] = t < a.N && x < a.D ? h[(size_t)t * a.D + x] : (uint16_t)0;
+  __syncthreads();
+  // this lane's (row, token) after the butterfly: the lane's upper kLog bits
+  const int mine = lane >> (5 - kLog), my_row = mine / T, my_token = mine % T;
+  const int y = my_token < a.N ? a.target[my_token] : a.ignore;
+  float m = -INFINITY, s = 0.0f;
+  const uint32_t total_warps = gridDim.x * kWarps;
+  for (uint32_t g = blockIdx.x * kWarps + warp; g < a.groups; g += total_warps) {
+    const uint32_t r = g / a.groups_per_rank;
+    const int row0 = (int)(g - r * a.groups_per_rank) * R, rows = a.rows[r];
+    const char *at[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)  // rows past the end read the last one; their results are dropped
+      at[i] = a.w[r] + (size_t)max(0, min(row0 + i, rows - 1)) * a.D * 2;
+    F2 acc[R][T];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int t = 0; t < T; ++t) acc[i][t] = F2{0.0f, 0.0f};
+    if constexpr (VEC) {
+      uint4 next[R];
+      if (lane * 8 < a.D) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) next[i] = ld_stream_v4(at[i] + lane * 16);
+      }
+      for (int x = lane * 8; x < a.D; x += 256) {
+        uint4 w[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) w[i] = next[i];
+        if (x + 256 < a.D) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) next[i] = ld_stream_v4(at[i] + (size_t)(x + 256) * 2);
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const uint4 hv = *reinterpret_cast<const uint4 *>(hs + t * a.dpad + x);
+          const uint32_t hq[4] = {hv.x, hv.y, hv.z, hv.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const F2 hp = pair_of(hq[q]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const uint32_t wq = q == 0 ? w[i].x : q == 1 ? w[i].y : q == 2 ? w[i].z : w[i].w;
+              acc[i][t] = fma2(pair_of(wq), hp, acc[i][t]);
+            }
+          }
+        }
+      }
+    } else {
+      for (int x = lane; x < a.D; x += 32) {
+        float w[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) w[i] = load_elem<BF16>(at[i], x);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const float hv = bf16_bits_to_f32(hs[t * a.dpad + x]);
+#pragma unroll
+          for (int i = 0; i < R; ++i) acc[i][t].x = fmaf(w[i], hv, acc[i][t].x);
+        }
+      }
+    }
+    float v[K];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int t = 0; t < T; ++t) v[i * T + t] = acc[i][t].x + acc[i][t].y;
+#pragma unroll
+    for (int d = 16, k = K; d > 0; d >>= 1) {
+      if (k > 1) {
+        k /= 2;
+        const bool upper = lane & d;
+#pragma unroll
+        for (int i = 0; i < K / 2; ++i) {
+          if (i < k) {
+            const float give = upper ? v[i] : v[i + k], keep = upper ? v[i + k] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+          }
+        }
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+      }
+    }
+    if (row0 + my_row < rows) {
+      const float z = v[0], nm = fmaxf(m, z);
+      if (y != a.ignore && y >= 0 && y == (int)r * a.C + row0 + my_row) a.ztarget[my_token] = z;
+      const float base = nm > -INFINITY ? nm * kLog2e : 0.0f;
+      s = fmaf(s, ex2(fmaf(m, kLog2e, -base)), ex2(fmaf(z, kLog2e, -base)));
+      m = nm;
+    }
+  }
+  // the lanes of one token (they differ in my_row), then the warps
+#pragma unroll
+  for (int d = 16; d >= 32 / R; d >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, d), os = __shfl_xor_sync(0xffffffffu, s, d);
+    const float nm = fmaxf(m, om), base = nm > -INFINITY ? nm * kLog2e : 0.0f;
+    s = s * ex2(fmaf(m, kLog2e, -base)) + os * ex2(fmaf(om, kLog2e, -base));
+    m = nm;
+  }
+  if (my_row == 0 && (lane & ((32 >> kLog) - 1)) == 0) wpart[warp][my_token] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x < a.N) {
+    float2 q = wpart[0][threadIdx.x];
+    for (int w = 1; w < kWarps; ++w) {
+      const float2 o = wpart[w][threadIdx.x];
+      const float nm = fmaxf(q.x, o.x), base = nm > -INFINITY ? nm * kLog2e : 0.0f;
+      q.y = q.y * ex2(fmaf(q.x, kLog2e, -base)) + o.y * ex2(fmaf(o.x, kLog2e, -base));
+      q.x = nm;
+    }
+    a.part[(size_t)blockIdx.x * a.N + threadIdx.x] = q;
   }
 }
 
@@ -605,6 +827,7 @@ int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 // How a problem is cut, and where its parts lie in the workspace.
 struct Plan {
   int C, tpr, ranks, tiles;       // rank pieces, 256-row tiles per rank, ranks with rows, all tiles
+  int few;                        // forward of few tokens: blocks of rc_ce_few_kernel (else 0)
   int dpad;
   int planes, per_piece, pieces;  // of the gradients' pass
   int splits, kper;
@@ -625,6 +848,14 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
     return here;
   };
   const size_t N = (size_t)s.tokens;
+  if (!backward && s.tokens <= kFewTokens && N * q.dpad * 2 <= kFewSmem) {
+    const int64_t groups = (int64_t)q.ranks * cdiv(q.C, 4);
+    q.few = (int)std::min<int64_t>(cdiv(groups, kThreads / 32), 2 * device_sm_count());
+    q.off_part = take((size_t)q.few * N * 8);
+    q.off_zt = take(N * 4);
+    q.bytes = at;
+    return q;
+  }
   if (copies || backward) q.off_h = take(N * q.dpad * 2);
   if (copies) q.off_w = take((size_t)q.ranks * q.C * q.dpad * 2);
   if (!backward) {
@@ -675,13 +906,43 @@ cudaError_t gemm(CeParams &a, cudaStream_t s) {
   return launch_kernel(rc_ce_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs)), dim3(kNT), smem_bytes(MODE), s, a);
 }
 
-cudaError_t pack(const void *src, void *dst, const int32_t *target, int64_t rows, int D, int dpad, int ignore,
+cudaError_t pack(const void *src, void *dst, const int32_t *target, int rows, int D, int dpad, int ignore,
                  cudaStream_t s) {
-  const int64_t n = rows * (dpad / 8);
+  const int64_t n = (int64_t)rows * (dpad / 8);
   const int64_t grid = std::min<int64_t>(cdiv(n, kThreads), (int64_t)device_sm_count() * 8);
-  return launch_kernel(rc_ce_pack_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
-                       static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), target, rows, D, dpad,
+  const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
+  return launch_kernel(vec ? rc_ce_pack_kernel<true> : rc_ce_pack_kernel<false>, dim3((unsigned)grid), dim3(kThreads),
+                       0, s, static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), target, rows, D, dpad,
                        ignore);
+}
+
+template <int T>
+cudaError_t few(const CeJob &j, const Plan &q, float2 *part, float *zt, cudaStream_t s) {
+  FewParams a{};
+  bool vec = j.shape.d % 8 == 0;
+  for (int r = 0; r < q.ranks; ++r) {
+    a.rows[r] = (int)std::min<int64_t>(q.C, j.shape.vocab - (int64_t)r * q.C);
+    a.w[r] = static_cast<const char *>(j.weight[r]);
+    vec = vec && reinterpret_cast<uintptr_t>(j.weight[r]) % 16 == 0;
+  }
+  a.h = static_cast<const char *>(j.hidden);
+  a.target = j.target;
+  a.part = part;
+  a.ztarget = zt;
+  a.N = (int)j.shape.tokens;
+  a.D = j.shape.d;
+  a.dpad = q.dpad;
+  a.C = q.C;
+  a.groups_per_rank = (uint32_t)cdiv(q.C, 4);
+  a.groups = a.groups_per_rank * q.ranks;
+  a.ignore = j.ignore;
+  const size_t smem = (size_t)T * q.dpad * 2;
+  auto kern = vec ? rc_ce_few_kernel<T, true> : rc_ce_few_kernel<T, false>;
+  if (smem > 48 * 1024) {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_kernel(kern, dim3((unsigned)q.few), dim3(kThreads), smem, s, a);
 }
 
 // Whether the tiled copies can read the caller's buffers (16-byte bases and
@@ -731,33 +992,44 @@ cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s) {
   const bool copies = copies_needed(j);
   const Plan q = make_plan(j.shape, false, copies);
   char *ws = static_cast<char *>(j.ws);
-  CeParams a{};
-  Operands o{};
-  cudaError_t err;
-  if ((err = operands(j, q, copies, &o, a.rows, s)) != cudaSuccess) return err;
-  const int D = j.shape.d;
+  float2 *const part = reinterpret_cast<float2 *>(ws + q.off_part);
+  float *const zt = reinterpret_cast<float *>(ws + q.off_zt);
   const int64_t N = j.shape.tokens;
-  if (!make_map(&a.a, o.h, 0, N, D, o.pitch, kHalf)) return cudaErrorInvalidValue;
-  for (int r = 0; r < q.ranks; ++r)
-    if (!make_map(&a.b[r], o.w[r], 0, a.rows[r], D, o.pitch, kHalf)) return cudaErrorInvalidValue;
-  a.target = j.target;
-  a.part = reinterpret_cast<float2 *>(ws + q.off_part);
-  a.ztarget = reinterpret_cast<float *>(ws + q.off_zt);
-  a.N = (int)N;
-  a.D = D;
-  a.C = q.C;
-  a.tpr = q.tpr;
-  a.ignore = j.ignore;
-  a.mt = (int)cdiv(N, kBM);
-  a.nt = q.tiles;
-  a.nk = (int)cdiv(D, kBK);
-  if ((err = gemm<kStats>(a, s)) != cudaSuccess) return err;
-  // as many rows per block as leave every thread of a row a tile or more
+  cudaError_t err;
+  int parts = q.tiles;
+  if (q.few) {
+    parts = q.few;
+    err = N == 1 ? few<1>(j, q, part, zt, s) : N == 2 ? few<2>(j, q, part, zt, s)
+        : N <= 4 ? few<4>(j, q, part, zt, s) : few<8>(j, q, part, zt, s);
+    if (err != cudaSuccess) return err;
+  } else {
+    CeParams a{};
+    Operands o{};
+    if ((err = operands(j, q, copies, &o, a.rows, s)) != cudaSuccess) return err;
+    const int D = j.shape.d;
+    bool ok = make_map(&a.a, o.h, 0, N, D, o.pitch, kHalf);
+    for (int r = 0; r < q.ranks; ++r) ok = ok && make_map(&a.b[r], o.w[r], 0, a.rows[r], D, o.pitch, kHalf);
+    if (!ok) return cudaErrorInvalidValue;
+    a.target = j.target;
+    a.part = part;
+    a.ztarget = zt;
+    a.N = (int)N;
+    a.D = D;
+    a.C = q.C;
+    a.tpr = q.tpr;
+    a.ignore = j.ignore;
+    a.mt = (int)cdiv(N, kBM);
+    a.nt = q.tiles;
+    a.nk = (int)cdiv(D, kBK);
+    a.chunk = kChunk;
+    if ((err = gemm<kStats>(a, s)) != cudaSuccess) return err;
+  }
+  // fewer rows per block (more blocks, more threads to a row) until the
+  // machine is full, as long as every thread has a part
   int lg = 5;
-  while (lg > 0 && ((kThreads >> lg) < q.tiles && (1 << (lg - 1)) >= N)) --lg;
-  return launch_kernel(rc_ce_join_kernel, dim3((unsigned)cdiv(N, 1 << lg)), dim3(kThreads), 0, s,
-                       (const float2 *)a.part, (const float *)a.ztarget, j.target, j.loss, j.lse, N,
-                       (int64_t)j.shape.vocab, q.tiles, lg, j.ignore);
+  while (lg > 0 && cdiv(N, 1 << lg) < device_sm_count() && (kThreads >> lg) < parts) --lg;
+  return launch_kernel(rc_ce_join_kernel, dim3((unsigned)cdiv(N, 1 << lg)), dim3(kThreads), 0, s, (const float2 *)part,
+                       (const float *)zt, j.target, j.loss, j.lse, N, (int64_t)j.shape.vocab, parts, lg, j.ignore);
 }
 
 cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
@@ -804,6 +1076,7 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
     z.mt = (int)cdiv(N, kBM);
     z.nt = nt;
     z.nk = (int)cdiv(D, kBK);
+    z.chunk = q.planes == 2 ? kChunk : z.nk;
     if ((err = gemm<kGrad>(z, s)) != cudaSuccess) return err;
     w.mt = nt;
     w.nt = (int)cdiv(D, kBN);

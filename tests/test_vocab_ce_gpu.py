@@ -133,6 +133,18 @@ def test_against_64_bits(rc, tokens, d, vocab, p):
     c.untouched()
 
 
+@pytest.mark.parametrize("tokens", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("d,vocab,p,shift", [(64, 3, 2, 0), (1, 9, 1, 0), (257, 1030, 5, 0), (4096, 4001, 8, 0), (512, 700, 3, 1), (20000, 333, 2, 0)])
+def test_few_tokens(rc, tokens, d, vocab, p, shift):
+    """Both sides of the border between the kernel for few tokens and the tiles."""
+    c = Case(tokens, d, vocab, p, seed=tokens, shift=shift)
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+    c.untouched()
+
+
 def test_vocabulary_in_several_pieces(rc):
     """G exceeds one piece of the workspace: dhidden adds over the pieces, the last one shorter."""
     c = Case(3000, 128, 20011, 4, seed=1)
