@@ -16,7 +16,9 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
+import struct
 from typing import Optional, Sequence, Union
 
 __all__ = [
@@ -93,14 +95,15 @@ _decl("rc_bucketer_flush", [_vp, _vp])
 _decl("rc_bucketer_destroy", [_vp])
 _decl("rc_all_to_all_v", [_vpp, _vpp, _i, ctypes.POINTER(ctypes.c_size_t), _i, _vp])
 _d, _u64, _i32 = ctypes.c_double, ctypes.c_uint64, ctypes.c_int32
-_decl("rc_dropout", [_vpp, _vpp, _vpp, _i, _sz, _i, _f, _d, _u64, _u64, _u64, _vp])
-_decl("rc_all_reduce_dropout", [_vpp, _vpp, _vpp, _i, _sz, _i, _f, _d, _u64, _u64, _vp])
+# pointer arrays of these are passed as bytes (see _typed_ptrs)
+_decl("rc_dropout", [_vp, _vp, _vp, _i, _sz, _i, _f, _d, _u64, _u64, _u64, _vp])
+_decl("rc_all_reduce_dropout", [_vp, _vp, _vp, _i, _sz, _i, _f, _d, _u64, _u64, _vp])
 _decl("rc_moe_gate_workspace", [_i, _i, _szp])
-_decl("rc_moe_gate", [_vpp, _vpp, _vpp, _vpp, _vpp, _vp, _vp, _i, _sz, _i, _i, _i, _i, _f, _vp, _sz, _vp])
-_decl("rc_moe_gate_backward", [_vpp, _vpp, _vpp, _vpp, _vp, _vp, _vpp, _i, _sz, _i, _i, _i, _i, _f, _vp])
+_decl("rc_moe_gate", [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _sz, _i, _i, _i, _i, _f, _vp, _sz, _vp])
+_decl("rc_moe_gate_backward", [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _sz, _i, _i, _i, _i, _f, _vp])
 _decl("rc_vocab_ce_workspace", [_sz, _sz, _sz, _i, _i, _i, _i, _szp])
-_decl("rc_vocab_ce_forward", [_vp, _vpp, _vp, _vp, _vp, _sz, _sz, _sz, _i, _i, _i32, _vp, _sz, _vp])
-_decl("rc_vocab_ce_backward", [_vp, _vpp, _vp, _vp, _vp, _vp, _vpp, _sz, _sz, _sz, _i, _i, _i32, _vp, _sz, _vp])
+_decl("rc_vocab_ce_forward", [_vp, _vp, _vp, _vp, _vp, _sz, _sz, _sz, _i, _i, _i32, _vp, _sz, _vp])
+_decl("rc_vocab_ce_backward", [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _sz, _sz, _i, _i, _i32, _vp, _sz, _vp])
 _decl("rc_rank_all_reduce", [_vpp, _vpp, _i, _i, _sz, _i, _i, _f, _vp])
 _decl("rc_rank_reduce_scatter", [_vpp, _vp, _i, _i, _sz, _i, _i, _i, _f, _vp])
 _decl("rc_rank_all_gather", [_vpp, _vp, _i, _i, _sz, _i, _vp])
@@ -448,10 +451,6 @@ class Bucketer:
 
 
 # ---------------------------------------------------------------- training-step operators
-def _opt_ptrs(xs):
-    return None if xs is None else _ptrs(xs)
-
-
 def _same_len(p: int, **lists) -> None:
     for name, xs in lists.items():
         if xs is not None and len(xs) != p:
@@ -475,27 +474,37 @@ def _typed(x, dtype, shape, what: str) -> Optional[int]:
     return x.data_ptr()
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _typed_ptrs(xs, dtype, shapes, what: str):
-    """A pointer array of _typed addresses; shapes: one for all, or a list of
-    one for each.  Buffers like the first one pass on their element count."""
+    """A pointer array (as bytes) of _typed addresses; shapes: one for all, or
+    a list of one for each.  With one shape, tensors after the first pass on
+    their type, element count and contiguity, checked for all at once."""
     if xs is None:
         return None
-    if isinstance(shapes, list):
-        return (ctypes.c_void_p * len(xs))(*[_typed(x, dtype, s, what) for x, s in zip(xs, shapes)])
-    out = [_typed(xs[0], dtype, shapes, what)]
-    tensor, first, n, dims = _torch_mod().Tensor, dtype[0] if dtype else None, math.prod(shapes), len(shapes)
-    for x in xs[1:]:
-        if type(x) is tensor and x.dtype is first and x.numel() == n and x.dim() == dims and x.is_contiguous():
-            out.append(x.data_ptr())
-        else:
-            out.append(_typed(x, dtype, shapes, what))
-    return (ctypes.c_void_p * len(out))(*out)
+    p = len(xs)
+    if not isinstance(shapes, list):
+        shapes = [shapes] * p
+        if p > 1 and dtype:
+            t = _torch_mod().Tensor
+            rest = xs[1:]
+            if list(map(type, rest)).count(t) == p - 1 and list(map(_dtype_of, rest)).count(dtype[0]) == p - 1 and \
+                    list(map(t.numel, rest)).count(math.prod(shapes[0])) == p - 1 and all(map(t.is_contiguous, rest)):
+                return struct.pack(f"{p}Q", _typed(xs[0], dtype, shapes[0], what), *map(t.data_ptr, rest))
+    return struct.pack(f"{p}Q", *[_typed(x, dtype, s, what) for x, s in zip(xs, shapes)])
+
+
+_kinds = None
 
 
 def _types():
-    """(float32, int32, byte masks) as sets of torch types, and the library's floating types by code."""
-    t = _torch_mod()
-    return (t.float32,), (t.int32,), (t.uint8, t.bool), {FP32: (t.float32,), BF16: (t.bfloat16,)}
+    """(float32, int32, byte masks) as tuples of torch types, and the library's floating types by code."""
+    global _kinds
+    if _kinds is None:
+        t = _torch_mod()
+        _kinds = (t.float32,), (t.int32,), (t.uint8, t.bool), {FP32: (t.float32,), BF16: (t.bfloat16,)}
+    return _kinds
 
 
 def _workspace(ws, nbytes: int, stream):
@@ -516,24 +525,47 @@ def _workspace(ws, nbytes: int, stream):
     return ws.data_ptr(), ws.numel(), ws
 
 
+def _flat_ptrs(xs, dtype, count: int, what: str):
+    """A pointer array (as bytes) of flat buffers of at least `count` elements."""
+    if xs is None:
+        return None
+    p, t = len(xs), _torch_mod().Tensor
+    if list(map(type, xs)).count(t) == p and list(map(_dtype_of, xs)).count(dtype[0] if dtype else None) == p and \
+            min(map(t.numel, xs)) >= count and all(map(t.is_contiguous, xs)):
+        return struct.pack(f"{p}Q", *map(t.data_ptr, xs))
+    for x in xs:
+        if _is_tensor(x) and (x.dtype not in dtype or x.numel() < count):
+            raise ValueError(f"{what} holds {x.numel()} elements of {x.dtype}; {count} of {dtype} are needed")
+    return struct.pack(f"{p}Q", *map(_addr, xs))
+
+
+def _dropout_buffers(send, recv, residual, n, dtype):
+    """(p, n, dtype code, the three pointer arrays); every buffer has send[0]'s type and n elements."""
+    p = len(send)
+    if len(recv) != p or (residual is not None and len(residual) != p):
+        _same_len(p, recv=recv, residual=residual)
+    dt = _dt(dtype, send[0])
+    count = _numel(send[0], n)
+    kind = _types()[3].get(dt, ())
+    ptrs = [_flat_ptrs(xs, kind, count, what) for xs, what in ((send, "send"), (recv, "recv"), (residual, "residual"))]
+    return p, count, dt, ptrs
+
+
 def rc_dropout(send: Sequence[Buf], recv: Sequence[Buf], prob: float, seed: int, offset: int = 0, rank_stride: int = 0,
                residual: Optional[Sequence[Buf]] = None, n=None, dtype=None, scale=1.0, stream=None):
     """recv[r] = residual[r] + dropout(scale * send[r]); the mask follows from
     seed and the index offset + r * rank_stride + i (see the header)."""
-    p = len(send)
-    _same_len(p, recv=recv, residual=residual)
-    _check(lib.rc_dropout(_ptrs(send), _opt_ptrs(residual), _ptrs(recv), p, _numel(send[0], n), _dt(dtype, send[0]),
-                          scale, prob, int(seed), int(offset), int(rank_stride), _stream(stream)), "rc_dropout")
+    p, n, dt, (src, dst, res) = _dropout_buffers(send, recv, residual, n, dtype)
+    _check(lib.rc_dropout(src, res, dst, p, n, dt, scale, prob, int(seed), int(offset), int(rank_stride),
+                          _stream(stream)), "rc_dropout")
 
 
 def rc_all_reduce_dropout(send: Sequence[Buf], recv: Sequence[Buf], prob: float, seed: int, offset: int = 0,
                           residual: Optional[Sequence[Buf]] = None, n=None, dtype=None, scale=1.0, stream=None):
     """recv[r] = residual[r] + dropout(scale * sum over the ranks of send), one
     mask for all ranks.  Its backward is rc_dropout with rank_stride 0."""
-    p = len(send)
-    _same_len(p, recv=recv, residual=residual)
-    _check(lib.rc_all_reduce_dropout(_ptrs(send), _opt_ptrs(residual), _ptrs(recv), p, _numel(send[0], n),
-                                     _dt(dtype, send[0]), scale, prob, int(seed), int(offset), _stream(stream)),
+    p, n, dt, (src, dst, res) = _dropout_buffers(send, recv, residual, n, dtype)
+    _check(lib.rc_all_reduce_dropout(src, res, dst, p, n, dt, scale, prob, int(seed), int(offset), _stream(stream)),
            "rc_all_reduce_dropout")
 
 

@@ -70,8 +70,7 @@ constexpr int kThreads = 256;  // of the small kernels
 enum Mode : int {
   kStats = 0,  // z tile -> (max, sum exp) per row, target logit
   kGrad = 1,   // z tile -> G tile
-  kDW = 2,     // G^T h -> dW rows
-  kDH = 3,     // G W -> fp32 sums
+  kBack = 2,   // G W -> dh (or fp32 sums of it), and G^T h -> dW rows
 };
 
 constexpr int stages(int mode) { return mode == kStats ? 6 : 5; }
@@ -79,47 +78,88 @@ constexpr uint32_t smem_bytes(int mode) {  // + slack to align to 1024
   return stages(mode) * kStageBytes + (mode == kStats ? 0u : kEpiWarps * kBoxBytes) + 1024u;
 }
 
+// The products of one launch: C[mt][nt] tiles, k in `splits` parts of `kper`
+// steps each.
+struct Shape {
+  int mt, nt, nk, kper;
+  uint32_t tiles;  // mt * nt * splits
+};
+
 struct alignas(64) CeParams {
-  CUtensorMap a;              // kStats, kGrad: h (K-major); kDW: G (64 x 64 boxes); kDH: G (K-major)
-  CUtensorMap b[kMaxRanks];   // kStats, kGrad: W_r (K-major); kDW: h (64 x 64 boxes, b[0]); kDH: W_r (64 x 64 boxes)
-  CUtensorMap out[kMaxRanks]; // kGrad: G (out[0]); kDW: dW_r; kDH: the sums (out[0])
+  CUtensorMap a;              // kStats, kGrad: h; kBack: G for dh (all K-major)
+  CUtensorMap b[kMaxRanks];   // W_r: K-major, or for dh in 64 x 64 boxes
+  CUtensorMap wa, wb;         // kBack: G and h for dW, 64 x 64 boxes
+  CUtensorMap out[kMaxRanks]; // kGrad: G (out[0]); kBack: dW_r
+  CUtensorMap dh;             // kBack: dh itself or the sums
   int rows[kMaxRanks];        // rows of each rank's piece
-  char *dw[kMaxRanks];        // kDW without dw_tma
+  char *dw[kMaxRanks];        // kBack without dw_tma
   const int32_t *target;
   const float *lse_in, *dloss;  // kGrad
   float2 *part;               // kStats: [tile][N]
   float *ztarget;             // kStats: [N]
+  const char *copy_from;      // kGrad: h to copy to copy_to, its ignored rows as zeros (or NULL)
+  char *copy_to;
+  Shape main, w;              // the logits or dh; dW
   int N, V;
   int D;
   int C;                      // rows of a full rank piece
   int tpr;                    // 256-row tiles per rank
   int j0;                     // first tile of this launch's piece
   int planes;                 // bf16 planes of G
-  int mt, nt, nk, kper, splits;
   int chunk;                  // kStats, kGrad: steps of k that one accumulator sums
-  uint32_t tiles;
+  int heavy, quota;           // kBack: the schedule (see tile_of)
   int ignore;
-  bool first;                 // kDH: store instead of add
-  bool dw_tma;                // kDW: rows are 16-byte multiples at 16-byte bases
+  bool first;                 // kBack: store the sums instead of adding to them
+  bool direct;                // kBack: dh is final
+  bool dw_tma;                // kBack: dW's rows are 16-byte multiples at 16-byte bases
 };
 
-struct TileAt {
-  int m, n, s;
+struct Tile {
+  int m, n, s, k0, k1;
+  bool dw;
 };
 
 // Tiles go in groups of kGroupM row tiles, all columns of a group before the
 // next group; the splits of k are outermost.
-__device__ __forceinline__ TileAt tile_at(const CeParams &a, uint32_t t) {
-  const uint32_t per = (uint32_t)a.mt * a.nt, gsz = (uint32_t)kGroupM * a.nt;
-  TileAt r;
-  r.s = (int)(t / per);
-  t -= r.s * per;
+__device__ __forceinline__ void place(const Shape &q, uint32_t t, Tile *r) {
+  const uint32_t per = (uint32_t)q.mt * q.nt, gsz = (uint32_t)kGroupM * q.nt;
+  r->s = (int)(t / per);
+  t -= r->s * per;
   const uint32_t g = t / gsz;
   t -= g * gsz;
-  const uint32_t gm = min((uint32_t)kGroupM, a.mt - g * kGroupM);
-  r.n = (int)(t / gm);
-  r.m = (int)(g * kGroupM + (t - r.n * gm));
-  return r;
+  const uint32_t gm = min((uint32_t)kGroupM, q.mt - g * kGroupM);
+  r->n = (int)(t / gm);
+  r->m = (int)(g * kGroupM + (t - r->n * gm));
+  r->k0 = r->s * q.kper;
+  r->k1 = min(q.nk, r->k0 + q.kper);
+}
+
+// The pair's i-th tile.  kBack: the long tiles of dh first, which some pairs
+// (`heavy` of them) have one more of; then `quota` tiles of dW for everybody,
+// and what is left of those for the other pairs, so that all end together.
+template <int MODE>
+__device__ __forceinline__ bool tile_of(const CeParams &a, uint32_t i, uint32_t pair, uint32_t pairs, Tile *r) {
+  const uint32_t t = i * pairs + pair;
+  r->dw = false;
+  if (t < a.main.tiles) {
+    place(a.main, t, r);
+    return true;
+  }
+  if constexpr (MODE == kBack) {
+    const uint32_t heavy = a.heavy, quota = a.quota;
+    const uint32_t j = i - (a.main.tiles / pairs + (pair < heavy ? 1 : 0));
+    uint32_t u = j * pairs + pair;
+    if (j >= quota) {
+      if (pair < heavy) return false;
+      u = quota * pairs + (j - quota) * (pairs - heavy) + (pair - heavy);
+    }
+    if (u < a.w.tiles) {
+      place(a.w, u, r);
+      r->dw = true;
+      return true;
+    }
+  }
+  return false;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -159,7 +199,7 @@ __device__ __forceinline__ uint32_t staging_unit(uint32_t box, int lane, int u) 
   return box + lane * 128 + ((u ^ (lane & 7)) << 4);
 }
 
-// kDH: where step kk of the piece's columns lies in the ranks' rows, and how
+// dh: where step kk of the piece's columns lies in the ranks' rows, and how
 // many steps are left in that rank's piece.
 __device__ __forceinline__ void dh_row(const CeParams &a, int kk, int *r, int *row, int *left) {
   const int per = a.tpr * (kBN / kBK), at = a.j0 * (kBN / kBK) + kk;
@@ -169,11 +209,22 @@ __device__ __forceinline__ void dh_row(const CeParams &a, int kk, int *r, int *r
   *left = per - in;
 }
 
+// h for the product with G, by the epilogue warps while they wait for the
+// first tile: what ignored rows hold must not meet their zeros in G (NaN * 0).
+__device__ __forceinline__ void copy_hidden(const CeParams &a) {
+  const uint32_t per = a.D / 8;  // 16-byte units of a row
+  const uint64_t n = (uint64_t)a.N * per;
+  for (uint64_t u = (uint64_t)blockIdx.x * (kEpiWarps * 32) + threadIdx.x; u < n;
+       u += (uint64_t)gridDim.x * (kEpiWarps * 32)) {
+    const uint32_t row = n >> 32 ? (uint32_t)(u / per) : (uint32_t)u / per;
+    const uint4 v = ld_stream_v4(a.copy_from + u * 16);
+    st_v4(a.copy_to + u * 16, a.target[row] == a.ignore ? make_uint4(0, 0, 0, 0) : v);
+  }
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     rc_ce_gemm_kernel(const __grid_constant__ CeParams a) {
-  constexpr bool A_MN = MODE == kDW;
-  constexpr bool B_MN = MODE == kDW || MODE == kDH;
   constexpr bool LOGITS = MODE == kStats || MODE == kGrad;
   constexpr uint32_t S = stages(MODE);
   extern __shared__ char smem_raw[];
@@ -218,26 +269,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
       uint32_t it = 0, slot = 0, phase = 0;
       bool ok = true, full_round = false;  // full_round: every slot has been filled once
       const uint32_t full0 = first_block_addr(&full[0]);
-      const int per_plane = LOGITS ? 0 : a.nk / a.planes;
-      for (uint32_t t = pair; ok && t < a.tiles; t += pairs) {
-        const TileAt w = tile_at(a, t);
-        const int k0 = w.s * a.kper, k1 = min(a.nk, k0 + a.kper);
+      Tile w;
+      for (uint32_t i = 0; ok && tile_of<MODE>(a, i, pair, pairs, &w); ++i) {
         const int am = w.m * kBM + (int)c * kHalf, bn = w.n * kBN + (int)c * kHalf;
         // what a step needs is carried from step to step: this thread has a few
         // hundred cycles for each, and a division would take most of them
         const CUtensorMap *bmap = &a.b[0];
-        int plane = 0, kk = k0, row = 0, left = 0, r = 0;
+        int plane = 0, kk = w.k0, row = 0, left = 0, r = 0, per_plane = 0;
         if constexpr (LOGITS) {
           const int j = a.j0 + w.n;
           r = j / a.tpr;
           bmap = &a.b[r];
           row = (j - r * a.tpr) * kBN + (int)c * kHalf;
         } else {
-          plane = k0 / per_plane;
-          kk = k0 - plane * per_plane;
-          if constexpr (MODE == kDH) dh_row(a, kk, &r, &row, &left);
+          per_plane = (w.dw ? a.w.nk : a.main.nk) / a.planes;
+          plane = kk / per_plane;
+          kk -= plane * per_plane;
+          if (!w.dw) dh_row(a, kk, &r, &row, &left);
         }
-        for (int k = k0; k < k1; ++k) {
+        for (int k = w.k0; k < w.k1; ++k) {
           if (full_round && !flow.wait(&empty[slot], phase ^ 1)) {
             ok = false;
             break;
@@ -250,10 +300,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             tma_load_2d(sa, &a.a, k * kBK, am, bar);
             tma_load_2d(sb, bmap, k * kBK, row, bar);
           } else {
-            if constexpr (MODE == kDW) {
+            if (w.dw) {
               row = kk * kBK;
-              tma_load_3d(sa, &a.a, am, row, plane, bar);
-              tma_load_3d(sa + 8192, &a.a, am + 64, row, plane, bar);
+              bmap = &a.wb;
+              tma_load_3d(sa, &a.wa, am, row, plane, bar);
+              tma_load_3d(sa + 8192, &a.wa, am + 64, row, plane, bar);
             } else {
               bmap = &a.b[r];
               tma_load_3d(sa, &a.a, kk * kBK, am, plane, bar);
@@ -261,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             tma_load_2d(sb, bmap, bn, row, bar);
             tma_load_2d(sb + 8192, bmap, bn + 64, row, bar);
             ++kk;
-            if constexpr (MODE == kDH) {
+            if (!w.dw) {
               row += kBK;
               if (--left == 0) {  // the next rank's piece
                 ++r;
@@ -272,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             if (kk == per_plane) {
               kk = 0;
               ++plane;
-              if constexpr (MODE == kDH) dh_row(a, 0, &r, &row, &left);
+              if (!w.dw) dh_row(a, 0, &r, &row, &left);
             }
           }
           if (++slot == S) {
@@ -293,15 +344,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
     if (lane == 0 && c == 0) {
-      constexpr uint32_t idesc = tc_idesc(kBM, kBN, A_MN, B_MN);
-      constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
       uint32_t slot = 0, phase = 0, i = 0;
       bool ok = true;
-      for (uint32_t t = pair; ok && t < a.tiles; t += pairs) {
-        const TileAt w = tile_at(a, t);
-        const int k0 = w.s * a.kper, k1 = min(a.nk, k0 + a.kper);
-        for (int kc = k0; ok && kc < k1; kc += LOGITS ? a.chunk : k1 - k0, ++i) {
-          const int ke = LOGITS ? min(k1, kc + a.chunk) : k1;
+      Tile w;
+      for (uint32_t n = 0; ok && tile_of<MODE>(a, n, pair, pairs, &w); ++n) {
+        // h and W as they lie are K-major for the logits; G is for dh, but W
+        // is not; neither is for dW
+        const bool a_mn = !LOGITS && w.dw, b_mn = !LOGITS;
+        const uint32_t idesc = a_mn ? tc_idesc(kBM, kBN, true, b_mn) : tc_idesc(kBM, kBN, false, b_mn);
+        const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        for (int kc = w.k0; ok && kc < w.k1; kc += LOGITS ? a.chunk : w.k1 - w.k0, ++i) {
+          const int ke = LOGITS ? min(w.k1, kc + a.chunk) : w.k1;
           const uint32_t acc = i & 1, d = tmem + acc * kBN;
           if (i >= 2 && !flow.wait(&acc_empty[acc], (i / 2 - 1) & 1)) {
             ok = false;
@@ -315,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             }
             tc_fence_after_sync();
             const uint32_t sa = smem0 + slot * kStageBytes, sb = sa + kOpBytes;
-            const uint64_t da = tc_desc(sa, A_MN ? 8192 : 16), db = tc_desc(sb, B_MN ? 8192 : 16);
+            const uint64_t da = tc_desc(sa, a_mn ? 8192 : 16), db = tc_desc(sb, b_mn ? 8192 : 16);
 #pragma unroll
             for (int q = 0; q < kBK / 16; ++q)
               tc_mma(d, da + q * a_step, db + q * b_step, idesc, k > kc || q > 0);
@@ -340,17 +393,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     const uint32_t src0 = tmem + quarter * 64 + ((uint32_t)(quad * 32) << 16);
     const uint32_t box = smem0 + S * kStageBytes + warp * kBoxBytes;
     const uint32_t acc_empty_addr = first_block_addr(&acc_empty[0]);
+    if (MODE == kGrad && a.copy_from != nullptr) copy_hidden(a);
     uint32_t i = 0, nth = 0;
     bool ok = true;
-    for (uint32_t t = pair; t < a.tiles; t += pairs, ++nth) {
-      const TileAt w = tile_at(a, t);
-      const int row0 = w.m * kBM + (int)c * kHalf + quad * 32;  // the warp's first row (kDW: column of G)
+    Tile w;
+    for (; tile_of<MODE>(a, nth, pair, pairs, &w); ++nth) {
+      const int row0 = w.m * kBM + (int)c * kHalf + quad * 32;  // the warp's first row (dW: column of G)
       const int row = row0 + lane;
       float z[64];
 #pragma unroll
       for (int q = 0; q < 64; ++q) z[q] = 0.0f;
       // the tile's sum, chunk by chunk
-      const int nc = LOGITS ? (a.nk + a.chunk - 1) / a.chunk : 1;
+      const int nc = LOGITS ? (a.main.nk + a.chunk - 1) / a.chunk : 1;
 #pragma unroll 1
       for (int u = 0; u < nc; ++u, ++i) {
         const uint32_t acc = i & 1;
@@ -453,32 +507,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             }
           }
         }
-      } else if constexpr (MODE == kDW) {
-        const int j = a.j0 + w.m, r = j / a.tpr;
-        const int v0 = (j - r * a.tpr) * kBN + (int)c * kHalf + quad * 32;  // the warp's first row of W_r
+      } else if (w.dw || a.direct) {
+        // bf16 rows of dW_r or of dh
         const int x0 = w.n * kBN + quarter * 64;
-        if (a.dw_tma) {
-          staging_free(lane);
+        int r = 0, v0 = row0, rows = a.N;
+        if (w.dw) {
+          const int j = a.j0 + w.m;
+          r = j / a.tpr;
+          v0 = (j - r * a.tpr) * kBN + (int)c * kHalf + quad * 32;
+          rows = a.rows[r];
+        }
+        staging_free(lane);
 #pragma unroll
-          for (int q = 0; q < 64; q += 8)
-            sts128(staging_unit(box, lane, q / 8),
-                   make_uint4(pack_bf16x2(z[q], z[q + 1]), pack_bf16x2(z[q + 2], z[q + 3]),
-                              pack_bf16x2(z[q + 4], z[q + 5]), pack_bf16x2(z[q + 6], z[q + 7])));
-          staging_ready();
-          if (lane == 0 && v0 < a.rows[r] && x0 < a.D) {
-            tma_store_2d(&a.out[r], x0, v0, box);
+        for (int q = 0; q < 64; q += 8)
+          sts128(staging_unit(box, lane, q / 8),
+                 make_uint4(pack_bf16x2(z[q], z[q + 1]), pack_bf16x2(z[q + 2], z[q + 3]),
+                            pack_bf16x2(z[q + 4], z[q + 5]), pack_bf16x2(z[q + 6], z[q + 7])));
+        staging_ready();
+        if (!w.dw || a.dw_tma) {
+          if (lane == 0 && v0 < rows && x0 < a.D) {
+            tma_store_2d(w.dw ? &a.out[r] : &a.dh, x0, v0, box);
             bulk_commit();
           }
-        } else {
-          // through the staging rows too, so that a warp's stores are neighbours
-          staging_free(lane);
-#pragma unroll
-          for (int q = 0; q < 64; q += 8)
-            sts128(staging_unit(box, lane, q / 8),
-                   make_uint4(pack_bf16x2(z[q], z[q + 1]), pack_bf16x2(z[q + 2], z[q + 3]),
-                              pack_bf16x2(z[q + 4], z[q + 5]), pack_bf16x2(z[q + 6], z[q + 7])));
-          __syncwarp();
-          const int n = min(32, a.rows[r] - v0);
+        } else {  // rows of any length and base: a warp's stores are neighbours
+          const int n = min(32, rows - v0);
           for (int e = 0; e < n; ++e) {
             uint16_t *out = reinterpret_cast<uint16_t *>(a.dw[r]) + (int64_t)(v0 + e) * a.D;
 #pragma unroll
@@ -504,8 +556,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           staging_ready();
           // one add per element and launch, launches in stream order: a fixed order
           if (lane == 0 && row0 < a.N && x0 + h * 32 < a.D) {
-            if (a.first) tma_store_3d(&a.out[0], x0 + h * 32, row0, w.s, box);
-            else tma_add_3d(&a.out[0], x0 + h * 32, row0, w.s, box);
+            if (a.first) tma_store_3d(&a.dh, x0 + h * 32, row0, w.s, box);
+            else tma_add_3d(&a.dh, x0 + h * 32, row0, w.s, box);
             bulk_commit();
           }
         }
@@ -870,10 +922,16 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
     q.pieces = (int)cdiv(q.tiles, std::min<int64_t>(want, q.tiles));
     q.per_piece = (int)cdiv(q.tiles, q.pieces);
     q.pieces = (int)cdiv(q.tiles, q.per_piece);
-    // few output tiles of dh: split its long k (the piece's columns)
+    // One launch makes dh and dW of a piece.  dh's tiles sum over the piece's
+    // columns, so with few of them one would outlast the rest: k is split until
+    // a part is no longer than a pair's share of all the steps (16 at least: a
+    // shorter part gains less than the extra launch that adds the parts costs).
+    const int64_t pairs = std::max(1, device_sm_count() / 2);
     const int64_t nk = (int64_t)q.planes * q.per_piece * (kBN / kBK);
     const int64_t out_tiles = cdiv(s.tokens, kBM) * cdiv(s.d, kBN);
-    int64_t sp = std::max<int64_t>(1, std::min<int64_t>(device_sm_count() / 2 / out_tiles, nk / 8));
+    const int64_t dw_steps = (int64_t)q.per_piece * cdiv(s.d, kBN) * q.planes * cdiv(s.tokens, kBK);
+    const int64_t share = std::max<int64_t>(16, (out_tiles * nk + dw_steps) / pairs);
+    const int64_t sp = std::max<int64_t>(1, std::min<int64_t>(cdiv(nk, share), cdiv(pairs, out_tiles)));
     q.kper = (int)cdiv(nk, sp);
     q.splits = (int)cdiv(nk, q.kper);
     q.off_g = take((size_t)q.planes * N * q.per_piece * kBN * 2);
@@ -881,6 +939,16 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
   }
   q.bytes = at;
   return q;
+}
+
+bool shape_of(Shape *q, int64_t mt, int64_t nt, int64_t nk, int64_t kper) {
+  q->mt = (int)mt;
+  q->nt = (int)nt;
+  q->nk = (int)nk;
+  q->kper = (int)kper;
+  const int64_t tiles = mt * nt * cdiv(nk, kper);
+  q->tiles = (uint32_t)tiles;
+  return tiles <= 0x20000000;  // (beyond what fits in memory)
 }
 
 template <int MODE>
@@ -895,14 +963,17 @@ cudaError_t gemm(CeParams &a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  if (a.splits < 1) {
-    a.splits = 1;
-    a.kper = a.nk;
+  const int64_t all = (int64_t)a.main.tiles + (MODE == kBack ? a.w.tiles : 0);
+  const int64_t pairs = std::min<int64_t>(all, device_sm_count() / 2);
+  if (MODE == kBack) {
+    // steps of k per pair, and how many of dW's tiles fit beside the longer
+    // share of dh's
+    a.heavy = (int)(a.main.tiles % pairs);
+    const double h = (double)a.main.kper, w = (double)a.w.nk + 1.0;  // + the tile's own overhead
+    const double share = ((double)a.main.tiles * h + (double)a.w.tiles * w) / (double)pairs;
+    const double room = share - (double)(a.main.tiles / pairs + (a.heavy ? 1 : 0)) * h;
+    a.quota = (int)std::max(0.0, std::ceil(room / w));
   }
-  const int64_t tiles = (int64_t)a.mt * a.nt * a.splits;
-  if (tiles > 0x40000000) return cudaErrorInvalidValue;  // (beyond what fits in memory)
-  a.tiles = (uint32_t)tiles;
-  const int64_t pairs = std::min<int64_t>(tiles, device_sm_count() / 2);
   return launch_kernel(rc_ce_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs)), dim3(kNT), smem_bytes(MODE), s, a);
 }
 
@@ -965,7 +1036,7 @@ cudaError_t operands(const CeJob &j, const Plan &q, bool copies, Operands *o, in
   cudaError_t err;
   o->pitch = copies ? q.dpad : j.shape.d;
   o->h = static_cast<const char *>(j.hidden);
-  if (copies || j.backward) {
+  if (copies) {
     if ((err = pack(j.hidden, ws + q.off_h, j.backward ? j.target : nullptr, j.shape.tokens, j.shape.d, q.dpad,
                     j.ignore, s)) != cudaSuccess)
       return err;
@@ -1018,9 +1089,7 @@ cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s) {
     a.C = q.C;
     a.tpr = q.tpr;
     a.ignore = j.ignore;
-    a.mt = (int)cdiv(N, kBM);
-    a.nt = q.tiles;
-    a.nk = (int)cdiv(D, kBK);
+    if (!shape_of(&a.main, cdiv(N, kBM), q.tiles, cdiv(D, kBK), cdiv(D, kBK))) return cudaErrorInvalidValue;
     a.chunk = kChunk;
     if ((err = gemm<kStats>(a, s)) != cudaSuccess) return err;
   }
@@ -1036,65 +1105,62 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
   const bool copies = copies_needed(j);
   const Plan q = make_plan(j.shape, true, copies);
   char *ws = static_cast<char *>(j.ws);
-  CeParams base{};
+  CeParams z{};  // the logits again, and G
   Operands o{};
   cudaError_t err;
-  if ((err = operands(j, q, copies, &o, base.rows, s)) != cudaSuccess) return err;
+  if ((err = operands(j, q, copies, &o, z.rows, s)) != cudaSuccess) return err;
   const int D = j.shape.d;
   const int64_t N = j.shape.tokens;
-  base.target = j.target;
-  base.lse_in = j.lse_in;
-  base.dloss = j.dloss;
   char *const g = ws + q.off_g;
   float *const sums = reinterpret_cast<float *>(ws + q.off_dh);
-  base.N = (int)N;
-  base.D = D;
-  base.C = q.C;
-  base.tpr = q.tpr;
-  base.planes = q.planes;
-  base.ignore = j.ignore;
-  base.V = (int)j.shape.vocab;
-  base.dw_tma = D % 8 == 0;
+  z.target = j.target;
+  z.lse_in = j.lse_in;
+  z.dloss = j.dloss;
+  z.N = (int)N;
+  z.D = D;
+  z.C = q.C;
+  z.tpr = q.tpr;
+  z.planes = q.planes;
+  z.ignore = j.ignore;
+  z.V = (int)j.shape.vocab;
+  z.chunk = q.planes == 2 ? kChunk : (int)cdiv(D, kBK);
+  CeParams w = z;  // dh and dW
+  w.dw_tma = D % 8 == 0;
   for (int r = 0; r < q.ranks; ++r) {
-    base.dw[r] = static_cast<char *>(j.dweight[r]);
-    base.dw_tma = base.dw_tma && reinterpret_cast<uintptr_t>(j.dweight[r]) % 16 == 0;
+    w.dw[r] = static_cast<char *>(j.dweight[r]);
+    w.dw_tma = w.dw_tma && reinterpret_cast<uintptr_t>(j.dweight[r]) % 16 == 0;
   }
-  CeParams z = base, w = base, h = base;
-  bool ok = make_map(&z.a, o.h, 0, N, D, q.dpad, kHalf) && make_map(&w.b[0], o.h, 0, N, D, q.dpad, 64) &&
-            make_map(&h.out[0], sums, q.splits, N, D, q.dpad, 32, true);
+  const bool dh_aligned = D % 8 == 0 && reinterpret_cast<uintptr_t>(j.dhidden) % 16 == 0;
+  w.direct = q.pieces == 1 && q.splits == 1 && dh_aligned;
+  const char *const h = ws + q.off_h;
+  bool ok = make_map(&z.a, o.h, 0, N, D, o.pitch, kHalf) && make_map(&w.wb, h, 0, N, D, q.dpad, 64) &&
+            (w.direct ? make_map(&w.dh, j.dhidden, 0, N, D, D, 32)
+                      : make_map(&w.dh, sums, q.splits, N, D, q.dpad, 32, true));
   for (int r = 0; r < q.ranks; ++r) {
-    ok = ok && make_map(&z.b[r], o.w[r], 0, base.rows[r], D, o.pitch, kHalf) &&
-         make_map(&h.b[r], o.w[r], 0, base.rows[r], D, o.pitch, 64);
-    if (base.dw_tma) ok = ok && make_map(&w.out[r], base.dw[r], 0, base.rows[r], D, D, 32);
+    ok = ok && make_map(&z.b[r], o.w[r], 0, z.rows[r], D, o.pitch, kHalf) &&
+         make_map(&w.b[r], o.w[r], 0, z.rows[r], D, o.pitch, 64);
+    if (w.dw_tma) ok = ok && make_map(&w.out[r], w.dw[r], 0, z.rows[r], D, D, 32);
   }
+  const int64_t mt = cdiv(N, kBM), dt = cdiv(D, kBN), nk = cdiv(D, kBK);
   for (int i = 0; ok && i < q.pieces; ++i) {
     const int j0 = i * q.per_piece, nt = std::min(q.per_piece, q.tiles - j0), cols = nt * kBN;
-    z.j0 = w.j0 = h.j0 = j0;
-    ok = make_map(&z.out[0], g, q.planes, N, cols, cols, 32) && make_map(&w.a, g, q.planes, N, cols, cols, 64) &&
-         make_map(&h.a, g, q.planes, N, cols, cols, kHalf);
+    z.j0 = w.j0 = j0;
+    ok = make_map(&z.out[0], g, q.planes, N, cols, cols, 32) && make_map(&w.wa, g, q.planes, N, cols, cols, 64) &&
+         make_map(&w.a, g, q.planes, N, cols, cols, kHalf) && shape_of(&z.main, mt, nt, nk, nk) &&
+         shape_of(&w.main, mt, dt, (int64_t)q.planes * cols / kBK, q.kper) &&
+         shape_of(&w.w, nt, dt, q.planes * cdiv(N, kBK), q.planes * cdiv(N, kBK));
     if (!ok) break;
-    z.mt = (int)cdiv(N, kBM);
-    z.nt = nt;
-    z.nk = (int)cdiv(D, kBK);
-    z.chunk = q.planes == 2 ? kChunk : z.nk;
+    z.copy_from = i == 0 && !copies ? o.h : nullptr;
+    z.copy_to = ws + q.off_h;
     if ((err = gemm<kGrad>(z, s)) != cudaSuccess) return err;
-    w.mt = nt;
-    w.nt = (int)cdiv(D, kBN);
-    w.nk = q.planes * (int)cdiv(N, kBK);
-    if ((err = gemm<kDW>(w, s)) != cudaSuccess) return err;
-    h.mt = (int)cdiv(N, kBM);
-    h.nt = (int)cdiv(D, kBN);
-    h.nk = q.planes * cols / kBK;
-    h.kper = q.kper;
-    h.splits = (int)cdiv(h.nk, q.kper);
-    h.first = i == 0;
-    if ((err = gemm<kDH>(h, s)) != cudaSuccess) return err;
+    w.first = i == 0;
+    if ((err = gemm<kBack>(w, s)) != cudaSuccess) return err;
   }
   if (!ok) return cudaErrorInvalidValue;
+  if (w.direct) return cudaSuccess;
   const int64_t grid = std::min<int64_t>(cdiv(N * (q.dpad / 8), kThreads), (int64_t)device_sm_count() * 8);
-  const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(j.dhidden) % 16 == 0;
   return launch_kernel(rc_ce_finish_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, (const float *)sums,
-                       static_cast<char *>(j.dhidden), N, D, q.dpad, q.splits, vec);
+                       static_cast<char *>(j.dhidden), N, D, q.dpad, q.splits, dh_aligned);
 }
 
 cudaError_t read_and_clear_ce_timeouts(unsigned int *count) {
