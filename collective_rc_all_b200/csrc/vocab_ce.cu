@@ -111,6 +111,7 @@ struct alignas(64) CeParams {
   int ignore;
   bool first;                 // kBack: store the sums instead of adding to them
   bool direct;                // kBack: dh is final
+  bool stacked;               // kBack: dh's row tile is the first plane of G over the second
   bool dw_tma;                // kBack: dW's rows are 16-byte multiples at 16-byte bases
 };
 
@@ -255,6 +256,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     dead_s = 0;
     mbar_init_fence();
   }
+  if (warp == kEpiWarps && lane == 0) {
+    prefetch_map(&a.a);
+    prefetch_map(&a.b[0]);
+    if (MODE == kBack) {
+      prefetch_map(&a.wa);
+      prefetch_map(&a.wb);
+    }
+  }
   if (warp == kEpiWarps + 1) tmem_alloc_all(&tmem_base_s);
   tc_fence_before_sync();
   __syncthreads();
@@ -282,9 +291,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           bmap = &a.b[r];
           row = (j - r * a.tpr) * kBN + (int)c * kHalf;
         } else {
-          per_plane = (w.dw ? a.w.nk : a.main.nk) / a.planes;
-          plane = kk / per_plane;
-          kk -= plane * per_plane;
+          if (!w.dw && a.stacked) {
+            per_plane = a.main.nk;
+            plane = (int)c;
+          } else {
+            per_plane = (w.dw ? a.w.nk : a.main.nk) / a.planes;
+            plane = kk / per_plane;
+            kk -= plane * per_plane;
+          }
           if (!w.dw) dh_row(a, kk, &r, &row, &left);
         }
         for (int k = w.k0; k < w.k1; ++k) {
@@ -307,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
               tma_load_3d(sa + 8192, &a.wa, am + 64, row, plane, bar);
             } else {
               bmap = &a.b[r];
-              tma_load_3d(sa, &a.a, kk * kBK, am, plane, bar);
+              tma_load_3d(sa, &a.a, kk * kBK, a.stacked ? 0 : am, plane, bar);
             }
             tma_load_2d(sb, bmap, bn, row, bar);
             tma_load_2d(sb + 8192, bmap, bn + 64, row, bar);
@@ -400,12 +414,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     for (; tile_of<MODE>(a, nth, pair, pairs, &w); ++nth) {
       const int row0 = w.m * kBM + (int)c * kHalf + quad * 32;  // the warp's first row (dW: column of G)
       const int row = row0 + lane;
+      // what the logits' tiles need of the row, fetched before the tile is there
+      int j = 0, cols = 64, ycol = -1;
+      bool live = false, zero = false;
+      float lse2 = 0.0f, g = 0.0f;
+      if constexpr (LOGITS) {
+        j = a.j0 + w.n;
+        const int r = j / a.tpr, v0 = (j - r * a.tpr) * kBN + quarter * 64;
+        cols = a.rows[r] - v0;  // of this warp's 64
+        live = row < a.N;
+        const int y = live ? a.target[row] : 0, yt = y - (r * a.C + v0);
+        // the target's column among this warp's, if it is one of them
+        ycol = (live && y != a.ignore && y >= 0 && yt >= 0 && yt < min(cols, 64)) ? yt : -1;
+        if constexpr (MODE == kGrad) {
+          lse2 = live ? a.lse_in[row] * kLog2e : 0.0f;
+          g = live ? a.dloss[row] : 0.0f;
+          // a label that is no word and not the ignored one poisons its row
+          if (y < 0 || y >= a.V) g = __int_as_float(0x7fc00000);
+          zero = !live || y == a.ignore;
+        }
+      }
+      // the tile, or its first chunk; then the other chunks are added
       float z[64];
-#pragma unroll
-      for (int q = 0; q < 64; ++q) z[q] = 0.0f;
-      // the tile's sum, chunk by chunk
       const int nc = LOGITS ? (a.main.nk + a.chunk - 1) / a.chunk : 1;
-#pragma unroll 1
       for (int u = 0; u < nc; ++u, ++i) {
         const uint32_t acc = i & 1;
         if (!__all_sync(0xffffffffu, flow.wait(&acc_full[acc], (i / 2) & 1))) {
@@ -413,12 +444,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           break;
         }
         tc_fence_after_sync();
+        if (u == 0) {
+          tmem_load64(src0 + acc * kBN, z);
+        } else {
 #pragma unroll
-        for (int q = 0; q < 64; q += 16) {
-          float v[16];
-          tmem_load16(src0 + acc * kBN + q, v);
+          for (int q = 0; q < 64; q += 16) {
+            float v[16];
+            tmem_load16(src0 + acc * kBN + q, v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) z[q + e] += v[e];
+            for (int e = 0; e < 16; ++e) z[q + e] += v[e];
+          }
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -426,39 +461,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
       }
       if (!ok) break;
       if constexpr (LOGITS) {
-        const int j = a.j0 + w.n, r = j / a.tpr, v0 = (j - r * a.tpr) * kBN;
-        const int cols = max(0, min(kBN, a.rows[r] - v0)) - quarter * 64;  // of this warp's 64
-        const bool live = row < a.N;
-        const int y = live ? a.target[row] : 0;
-        const int yt = y - (r * a.C + v0 + quarter * 64);
-        // the target's column among this warp's, if it is one of them
-        const int ycol = (y != a.ignore && y >= 0 && yt >= 0 && yt < min(cols, 64)) ? yt : -1;
-        if constexpr (MODE == kStats) {
-          if (cols < 64) {
+        if (cols < 64) {
 #pragma unroll
-            for (int q = 0; q < 64; ++q) z[q] = q < cols ? z[q] : -INFINITY;
-          }
+          for (int q = 0; q < 64; ++q) z[q] = q < cols ? z[q] : -INFINITY;
+        }
+        if constexpr (MODE == kStats) {
           if (ycol >= 0) {
             float zt = 0.0f;
 #pragma unroll
             for (int q = 0; q < 64; ++q) zt = ycol == q ? z[q] : zt;
             a.ztarget[row] = zt;
           }
-          float m = z[0];
+          float mq[4] = {z[0], z[1], z[2], z[3]};  // four chains each: short waits
 #pragma unroll
-          for (int q = 1; q < 64; ++q) m = fmaxf(m, z[q]);
+          for (int q = 4; q < 64; ++q) mq[q & 3] = fmaxf(mq[q & 3], z[q]);
+          const float m = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
           const float base = m > -INFINITY ? m * kLog2e : 0.0f;
-          float s0 = 0.0f, s1 = 0.0f;
+          float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int q = 0; q < 64; q += 2) {
-            s0 += ex2(fmaf(z[q], kLog2e, -base));
-            s1 += ex2(fmaf(z[q + 1], kLog2e, -base));
-          }
+          for (int q = 0; q < 64; ++q) sq[q & 3] += ex2(fmaf(z[q], kLog2e, -base));
           // the four warps of these rows; the first one writes the tile's pair
           if (quarter != 0 && nth > 0 &&
               !__all_sync(0xffffffffu, flow.wait(&join_free[quad], (nth - 1) & 1)))
             break;
-          join[quarter][row_l] = make_float2(m, s0 + s1);
+          join[quarter][row_l] = make_float2(m, (sq[0] + sq[1]) + (sq[2] + sq[3]));
           __syncwarp();
           if (lane == 0) mbar_arrive(&joined[quad]);
           if (quarter == 0) {
@@ -476,16 +502,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
             if (live) a.part[(size_t)j * a.N + row] = make_float2(nm, s);
           }
         } else {
-          const float lse2 = live ? a.lse_in[row] * kLog2e : 0.0f;
-          float g = live ? a.dloss[row] : 0.0f;
-          // a label that is no word and not the ignored one poisons its row
-          if (y < 0 || y >= a.V) g = __int_as_float(0x7fc00000);
-          const bool zero = !live || y == a.ignore;
 #pragma unroll
-          for (int q = 0; q < 64; ++q) {
-            float pr = ex2(fmaf(z[q], kLog2e, -lse2));
-            pr -= q == ycol ? 1.0f : 0.0f;
-            z[q] = (zero || q >= cols) ? 0.0f : pr * g;
+          for (int q = 0; q < 64; ++q) z[q] = ex2(fmaf(z[q], kLog2e, -lse2)) * g;
+          if (__any_sync(0xffffffffu, ycol >= 0)) {
+#pragma unroll
+            for (int q = 0; q < 64; ++q) z[q] -= q == ycol ? g : 0.0f;
           }
           for (int plane = 0; plane < a.planes; ++plane) {
             staging_free(lane);
@@ -494,11 +515,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
               uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                h[e] = pack_bf16x2(z[q + 2 * e], z[q + 2 * e + 1]);
-                z[q + 2 * e] -= __uint_as_float(h[e] << 16);  // what the next plane holds
-                z[q + 2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+                const uint32_t v = pack_bf16x2(z[q + 2 * e], z[q + 2 * e + 1]);
+                h[e] = zero ? 0u : v;  // whatever the row holds
               }
               sts128(staging_unit(box, lane, q / 8), make_uint4(h[0], h[1], h[2], h[3]));
+              if (plane + 1 < a.planes) {  // what the next plane holds
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  z[q + 2 * e] -= __uint_as_float(h[e] << 16);
+                  z[q + 2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+                }
+              }
             }
             staging_ready();
             if (lane == 0 && row0 < a.N) {
@@ -555,9 +582,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
                               __float_as_uint(z[h * 32 + q + 2]), __float_as_uint(z[h * 32 + q + 3])));
           staging_ready();
           // one add per element and launch, launches in stream order: a fixed order
-          if (lane == 0 && row0 < a.N && x0 + h * 32 < a.D) {
-            if (a.first) tma_store_3d(&a.dh, x0 + h * 32, row0, w.s, box);
-            else tma_add_3d(&a.dh, x0 + h * 32, row0, w.s, box);
+          const int y0 = a.stacked ? quad * 32 : row0, slot = a.stacked ? w.s * 2 + (int)c : w.s;
+          if (lane == 0 && y0 < a.N && x0 + h * 32 < a.D) {
+            if (a.first) tma_store_3d(&a.dh, x0 + h * 32, y0, slot, box);
+            else tma_add_3d(&a.dh, x0 + h * 32, y0, slot, box);
             bulk_commit();
           }
         }
@@ -612,50 +640,53 @@ __global__ void __launch_bounds__(kThreads) rc_ce_join_kernel(const float2 *part
   }
 }
 
-// dst[row][0, dpad) = src[row][0, D), zero behind D, and zero in rows whose
-// target is ignored (target NULL: none), so that whatever a padded row holds
-// stays out of the products.  VEC: src's rows are 16-byte multiples.
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) rc_ce_pack_kernel(const uint16_t *src, uint16_t *dst, const int32_t *target,
-                                                              int rows, int D, int dpad, int ignore) {
+// dst[row][0, dpad) = the ranks' rows one after the other (C to a rank), zero
+// behind D, and zero in rows whose target is ignored (target NULL: none), so
+// that whatever a padded row holds stays out of the products.
+struct PackParams {
+  const uint16_t *src[kMaxRanks];
+  uint16_t *dst;
+  const int32_t *target;
+  uint32_t rows, C;
+  int D, dpad, ignore;
+};
+
+__global__ void __launch_bounds__(kThreads) rc_ce_pack_kernel(const __grid_constant__ PackParams a) {
   pdl_wait();
-  const uint32_t per = dpad / 8;
-  const uint64_t n = (uint64_t)rows * per;
+  const uint32_t per = a.dpad / 8;
+  const uint64_t n = (uint64_t)a.rows * per;
   for (uint64_t u = (uint64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (uint64_t)gridDim.x * kThreads) {
-    const uint32_t row = n >> 32 ? (uint32_t)(u / per) : (uint32_t)u / per;
+    const uint32_t row = n >> 32 ? (uint32_t)(u / per) : (uint32_t)u / per, r = row / a.C;
     const int c = (int)(u - (uint64_t)row * per) * 8;
-    const bool skip = target != nullptr && target[row] == ignore;
-    const uint16_t *at = src + (size_t)row * D;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if constexpr (VEC) {
-      if (!skip) v = ld_stream_v4(at + c);
-    } else {
-      uint32_t w[4];
+    const bool skip = a.target != nullptr && a.target[row] == a.ignore;
+    const uint16_t *at = a.src[r] + (size_t)(row - r * a.C) * a.D;
+    uint32_t w[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int x = c + 2 * q;
-        const uint32_t lo = !skip && x < D ? at[x] : 0u;
-        const uint32_t hi = !skip && x + 1 < D ? at[x + 1] : 0u;
-        w[q] = lo | (hi << 16);
-      }
-      v = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int q = 0; q < 4; ++q) {
+      const int x = c + 2 * q;
+      const uint32_t lo = !skip && x < a.D ? at[x] : 0u;
+      const uint32_t hi = !skip && x + 1 < a.D ? at[x + 1] : 0u;
+      w[q] = lo | (hi << 16);
     }
-    st_v4(dst + (size_t)row * dpad + c, v);
+    st_v4(a.dst + (size_t)row * a.dpad + c, make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
 
 // ---------------------------------------------------------------- few tokens
 // The forward pass of up to kFewTokens tokens reads the weights once and does
 // little with them, so it is bound by that read; tensor-core tiles of 256 rows
-// would be nearly empty and take longer than the read.  A warp takes four rows
-// of W at a time, every lane 8 columns of each: 4 loads of 16 bytes (the next
-// 256 columns' four in flight meanwhile), 8 fp32 products per row and token in
-// pairs (fma.rn.f32x2).  The tokens' hidden rows lie in shared memory as bf16.
-// The four rows' sums of all tokens are reduced over the lanes in one
-// butterfly that leaves each (row, token) in a lane of its own, which keeps
-// the token's running maximum and sum of exponentials over the rows it sees.
-constexpr int kFewTokens = 8;
+// would be nearly empty and take longer than the read.  A warp takes R rows of
+// W at a time (8, or 4 with four tokens), every lane 8 columns of each: R loads
+// of 16 bytes, the next 256 columns' R in flight meanwhile, and 8 fp32 products
+// per row and token in pairs (fma.rn.f32x2).  The tokens' hidden rows lie in
+// shared memory as bf16.  The R rows' sums of all tokens are reduced over the
+// lanes in one butterfly that leaves each (row, token) in a lane of its own,
+// which keeps the token's running maximum and sum of exponentials over the rows
+// it sees.  More tokens are the tiles' (32000 x 4096, 5 tokens: 85 us here in
+// the same form, 68 us there; 4 tokens: 60 us here).
+constexpr int kFewTokens = 4;
 constexpr uint32_t kFewSmem = 96 * 1024;  // two blocks per SM
+constexpr int few_rows(int t) { return t <= 2 ? 8 : 4; }
 
 struct FewParams {
   const char *w[kMaxRanks];
@@ -665,7 +696,7 @@ struct FewParams {
   float2 *part;     // [block][N]
   float *ztarget;   // [N]
   int N, D, dpad, C;
-  uint32_t groups_per_rank, groups;  // groups of four rows
+  uint32_t groups_per_rank, groups;  // groups of few_rows rows
   int ignore;
 };
 
@@ -688,8 +719,8 @@ __device__ __forceinline__ F2 pair_of(uint32_t bf16x2) {
 // T: tokens, padded to a power of two.  VEC: rows of W are 16-byte multiples.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) rc_ce_few_kernel(const __grid_constant__ FewParams a) {
-  constexpr int R = 4, K = R * T;
-  constexpr int kLog = K == 4 ? 2 : K == 8 ? 3 : K == 16 ? 4 : 5;
+  constexpr int R = few_rows(T), K = R * T;
+  constexpr int kLog = K == 8 ? 3 : 4;
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint16_t hs[];  // [T][dpad]
   __shared__ float2 wpart[kWarps][T];
@@ -882,7 +913,8 @@ struct Plan {
   int few;                        // forward of few tokens: blocks of rc_ce_few_kernel (else 0)
   int dpad;
   int planes, per_piece, pieces;  // of the gradients' pass
-  int splits, kper;
+  int splits, kper, slots;        // of dh's k; sums kept (one or two per split)
+  bool stacked;
   size_t off_part, off_zt, off_h, off_w, off_g, off_dh, bytes;
 };
 
@@ -901,7 +933,7 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
   };
   const size_t N = (size_t)s.tokens;
   if (!backward && s.tokens <= kFewTokens && N * q.dpad * 2 <= kFewSmem) {
-    const int64_t groups = (int64_t)q.ranks * cdiv(q.C, 4);
+    const int64_t groups = (int64_t)q.ranks * cdiv(q.C, few_rows((int)N));
     q.few = (int)std::min<int64_t>(cdiv(groups, kThreads / 32), 2 * device_sm_count());
     q.off_part = take((size_t)q.few * N * 8);
     q.off_zt = take(N * 4);
@@ -927,15 +959,20 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
     // a part is no longer than a pair's share of all the steps (16 at least: a
     // shorter part gains less than the extra launch that adds the parts costs).
     const int64_t pairs = std::max(1, device_sm_count() / 2);
-    const int64_t nk = (int64_t)q.planes * q.per_piece * (kBN / kBK);
+    // Two planes are two halves of dh's k, or (N <= 128) the two halves of its
+    // row tile: half the steps, for sums that a launch must add up.  64 steps
+    // are about 16 us.
+    q.stacked = q.planes == 2 && q.planes * q.per_piece * (kBN / kBK) > 64;
+    const int64_t nk = (int64_t)(q.stacked ? 1 : q.planes) * q.per_piece * (kBN / kBK);
     const int64_t out_tiles = cdiv(s.tokens, kBM) * cdiv(s.d, kBN);
     const int64_t dw_steps = (int64_t)q.per_piece * cdiv(s.d, kBN) * q.planes * cdiv(s.tokens, kBK);
     const int64_t share = std::max<int64_t>(16, (out_tiles * nk + dw_steps) / pairs);
     const int64_t sp = std::max<int64_t>(1, std::min<int64_t>(cdiv(nk, share), cdiv(pairs, out_tiles)));
     q.kper = (int)cdiv(nk, sp);
     q.splits = (int)cdiv(nk, q.kper);
+    q.slots = q.splits * (q.stacked ? 2 : 1);
     q.off_g = take((size_t)q.planes * N * q.per_piece * kBN * 2);
-    q.off_dh = take((size_t)q.splits * N * q.dpad * 4);
+    q.off_dh = take((size_t)q.slots * N * q.dpad * 4);
   }
   q.bytes = at;
   return q;
@@ -977,14 +1014,11 @@ cudaError_t gemm(CeParams &a, cudaStream_t s) {
   return launch_kernel(rc_ce_gemm_kernel<MODE>, dim3((unsigned)(2 * pairs)), dim3(kNT), smem_bytes(MODE), s, a);
 }
 
-cudaError_t pack(const void *src, void *dst, const int32_t *target, int rows, int D, int dpad, int ignore,
-                 cudaStream_t s) {
-  const int64_t n = (int64_t)rows * (dpad / 8);
+cudaError_t pack(PackParams &a, int dpad, cudaStream_t s) {
+  a.dpad = dpad;
+  const int64_t n = (int64_t)a.rows * (dpad / 8);
   const int64_t grid = std::min<int64_t>(cdiv(n, kThreads), (int64_t)device_sm_count() * 8);
-  const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
-  return launch_kernel(vec ? rc_ce_pack_kernel<true> : rc_ce_pack_kernel<false>, dim3((unsigned)grid), dim3(kThreads),
-                       0, s, static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), target, rows, D, dpad,
-                       ignore);
+  return launch_kernel(rc_ce_pack_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, a);
 }
 
 template <int T>
@@ -1004,7 +1038,7 @@ cudaError_t few(const CeJob &j, const Plan &q, float2 *part, float *zt, cudaStre
   a.D = j.shape.d;
   a.dpad = q.dpad;
   a.C = q.C;
-  a.groups_per_rank = (uint32_t)cdiv(q.C, 4);
+  a.groups_per_rank = (uint32_t)cdiv(q.C, few_rows(T));
   a.groups = a.groups_per_rank * q.ranks;
   a.ignore = j.ignore;
   const size_t smem = (size_t)T * q.dpad * 2;
@@ -1036,20 +1070,25 @@ cudaError_t operands(const CeJob &j, const Plan &q, bool copies, Operands *o, in
   cudaError_t err;
   o->pitch = copies ? q.dpad : j.shape.d;
   o->h = static_cast<const char *>(j.hidden);
-  if (copies) {
-    if ((err = pack(j.hidden, ws + q.off_h, j.backward ? j.target : nullptr, j.shape.tokens, j.shape.d, q.dpad,
-                    j.ignore, s)) != cudaSuccess)
-      return err;
-    o->h = ws + q.off_h;
-  }
+  PackParams hp{}, wp{};
   for (int r = 0; r < q.ranks; ++r) {
     rows[r] = (int)std::min<int64_t>(q.C, j.shape.vocab - (int64_t)r * q.C);
+    wp.src[r] = static_cast<const uint16_t *>(j.weight[r]);
     o->w[r] = static_cast<const char *>(j.weight[r]);
-    if (copies) {
-      char *dst = ws + q.off_w + (size_t)r * q.C * q.dpad * 2;
-      if ((err = pack(j.weight[r], dst, nullptr, rows[r], j.shape.d, q.dpad, 0, s)) != cudaSuccess) return err;
-      o->w[r] = dst;
-    }
+    if (copies) o->w[r] = ws + q.off_w + (size_t)r * q.C * q.dpad * 2;
+  }
+  if (copies) {
+    hp.src[0] = static_cast<const uint16_t *>(j.hidden);
+    hp.dst = reinterpret_cast<uint16_t *>(ws + q.off_h);
+    hp.target = j.backward ? j.target : nullptr;
+    hp.rows = hp.C = (uint32_t)j.shape.tokens;
+    wp.dst = reinterpret_cast<uint16_t *>(ws + q.off_w);
+    wp.rows = (uint32_t)j.shape.vocab;
+    wp.C = (uint32_t)q.C;
+    hp.D = wp.D = j.shape.d;
+    hp.ignore = j.ignore;
+    if ((err = pack(hp, q.dpad, s)) != cudaSuccess || (err = pack(wp, q.dpad, s)) != cudaSuccess) return err;
+    o->h = ws + q.off_h;
   }
   return cudaSuccess;
 }
@@ -1070,8 +1109,7 @@ cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s) {
   int parts = q.tiles;
   if (q.few) {
     parts = q.few;
-    err = N == 1 ? few<1>(j, q, part, zt, s) : N == 2 ? few<2>(j, q, part, zt, s)
-        : N <= 4 ? few<4>(j, q, part, zt, s) : few<8>(j, q, part, zt, s);
+    err = N == 1 ? few<1>(j, q, part, zt, s) : N == 2 ? few<2>(j, q, part, zt, s) : few<4>(j, q, part, zt, s);
     if (err != cudaSuccess) return err;
   } else {
     CeParams a{};
@@ -1131,11 +1169,12 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
     w.dw_tma = w.dw_tma && reinterpret_cast<uintptr_t>(j.dweight[r]) % 16 == 0;
   }
   const bool dh_aligned = D % 8 == 0 && reinterpret_cast<uintptr_t>(j.dhidden) % 16 == 0;
-  w.direct = q.pieces == 1 && q.splits == 1 && dh_aligned;
+  w.direct = q.pieces == 1 && q.slots == 1 && dh_aligned;
+  w.stacked = q.stacked;
   const char *const h = ws + q.off_h;
   bool ok = make_map(&z.a, o.h, 0, N, D, o.pitch, kHalf) && make_map(&w.wb, h, 0, N, D, q.dpad, 64) &&
             (w.direct ? make_map(&w.dh, j.dhidden, 0, N, D, D, 32)
-                      : make_map(&w.dh, sums, q.splits, N, D, q.dpad, 32, true));
+                      : make_map(&w.dh, sums, q.slots, N, D, q.dpad, 32, true));
   for (int r = 0; r < q.ranks; ++r) {
     ok = ok && make_map(&z.b[r], o.w[r], 0, z.rows[r], D, o.pitch, kHalf) &&
          make_map(&w.b[r], o.w[r], 0, z.rows[r], D, o.pitch, 64);
@@ -1147,7 +1186,7 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
     z.j0 = w.j0 = j0;
     ok = make_map(&z.out[0], g, q.planes, N, cols, cols, 32) && make_map(&w.wa, g, q.planes, N, cols, cols, 64) &&
          make_map(&w.a, g, q.planes, N, cols, cols, kHalf) && shape_of(&z.main, mt, nt, nk, nk) &&
-         shape_of(&w.main, mt, dt, (int64_t)q.planes * cols / kBK, q.kper) &&
+         shape_of(&w.main, mt, dt, (int64_t)(q.stacked ? 1 : q.planes) * cols / kBK, q.kper) &&
          shape_of(&w.w, nt, dt, q.planes * cdiv(N, kBK), q.planes * cdiv(N, kBK));
     if (!ok) break;
     z.copy_from = i == 0 && !copies ? o.h : nullptr;
@@ -1160,7 +1199,7 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
   if (w.direct) return cudaSuccess;
   const int64_t grid = std::min<int64_t>(cdiv(N * (q.dpad / 8), kThreads), (int64_t)device_sm_count() * 8);
   return launch_kernel(rc_ce_finish_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, (const float *)sums,
-                       static_cast<char *>(j.dhidden), N, D, q.dpad, q.splits, dh_aligned);
+                       static_cast<char *>(j.dhidden), N, D, q.dpad, q.slots, dh_aligned);
 }
 
 cudaError_t read_and_clear_ce_timeouts(unsigned int *count) {
