@@ -172,9 +172,9 @@ __device__ __forceinline__ float ex2(float x) {
 struct Flow {
   volatile uint32_t *dead;
   __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait_cluster(bar, parity)) {
+    while (!mbar_try_wait(bar, parity)) {
       if (*dead) return false;
       if (global_ns() - t0 > kWaitLimitNs) {
         if (atomicExch(const_cast<uint32_t *>(dead), 1u) == 0) atomicAdd(&g_wait_timeouts_ce, 1u);
