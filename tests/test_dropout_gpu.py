@@ -97,7 +97,7 @@ def test_every_phase_of_the_index_and_misaligned_buffers(rc, dt, offset):
     n, p, seed = 1000, 2, 2**64 - 3
     xs = rc_inputs.normal(p, n, seed=3, dt=dt)
     want = expect(xs, xs, n, dt, 0.5, seed, offset, 17, 1.0)
-    for shift in (0, ESZ[dt]):
+    for shift in (0, 16, ESZ[dt]):
         d, _ = to_dev(xs, dt, offset_bytes=shift)
         e, _ = to_dev(xs, dt, offset_bytes=shift)
         y, back = empty_dev(n, dt, p, offset_bytes=shift)
@@ -180,7 +180,7 @@ def test_all_reduce_dropout(rc, dt, p, n, res):
     total = ring_fold([widen(x, dt) for x in xs], n, p)
     k = keep(offset, n, seed, prob)
     v = np.where(k, total * factor(prob, 0.25), np.float32(0))
-    for shift in (0, ESZ[dt]):
+    for shift in (0, 16, ESZ[dt]):
         d, _ = to_dev(xs, dt, offset_bytes=shift)
         e = to_dev(rs, dt, offset_bytes=shift)[0] if res else None
         y, back = empty_dev(n, dt, p, offset_bytes=shift)
