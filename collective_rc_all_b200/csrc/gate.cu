@@ -15,16 +15,16 @@
 // A token's row lies in the registers of LPT lanes, VPL values each (a lane
 // owns VPL neighbouring experts), so a warp works on 32 / LPT tokens at once
 // and every reduction over a row is log2(LPT) shuffles (one redux for whole
-// warps).  The top k come from rounds over the lanes' best values; a lane
-// keeps its two best at hand and looks through its row again only when it
-// wins a third time.  The sums over tokens (P_e, counts) stay in registers
-// while a block walks its tokens and leave it as one partial per block; a
+// warps).  The top k come from rounds over the lanes' best values (see pick).
+// The sums over tokens (P_e in registers, counts in shared memory) stay with a
+// block while it walks its tokens and leave it as one partial per block; a
 // second launch (one cluster of 8 blocks, each an eighth of the experts) adds
 // the partials in block order, so the results are the same on every run (no
 // floating-point atomics).  Few tokens are one block's work altogether, in
 // one launch.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "bulk.cuh"
 #include "common.cuh"
@@ -84,13 +84,13 @@ __device__ __forceinline__ void load_row(const char *row, int e0, int E, bool ve
   }
 }
 
-// The same for token t of a rank; nothing but -inf when there is no such token
-// or it is masked.
+// The same for token t of a rank, whose row is at `row`; nothing but -inf when
+// there is no such token or it is masked.
 template <class T, int VPL>
-__device__ __forceinline__ void load_token(const GateParams &a, const char *rows, const uint8_t *mask, uint64_t t,
+__device__ __forceinline__ void load_token(const GateParams &a, const char *row, const uint8_t *mask, uint64_t t,
                                            int e0, float (&z)[VPL]) {
   if (t < a.tokens && (mask == nullptr || mask[t] != 0)) {
-    load_row<T, VPL>(rows + t * (uint64_t)a.E * T::kBytes, e0, a.E, a.vec, z);
+    load_row<T, VPL>(row, e0, a.E, a.vec, z);
   } else {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) z[j] = -INFINITY;
@@ -152,7 +152,7 @@ __device__ __forceinline__ float row_exp(const float (&z)[VPL], float top, float
 }
 
 // What a block holds of its tokens: each expert's probabilities (a lane's
-// experts) and choices (in shared memory, added by the lanes that win them).
+// experts); the choices are counted in shared memory.
 template <int VPL>
 struct Sums {
   float p[VPL];
@@ -161,102 +161,197 @@ struct Sums {
 
 template <int LPT>
 struct Slots {  // the chosen experts of the tokens that a warp is at
-  static constexpr int kSlots = LPT == 1 ? 8 : kMaxK;  // 8 experts at most have a lane per token
-  int32_t id[32 / LPT][kSlots];
-  float z[32 / LPT][kSlots];
+  static constexpr int kSlots = LPT == 1 ? 8 : kMaxK + 1;  // 8 experts at most have a lane per token
+  int32_t id[32 / LPT][kSlots];  // -1: none (pick: the key; 0: none)
+  float z[32 / LPT][kSlots];     // pick_exact only
 };
 
-// The tokens of rank r that fall to this block.
-template <class T, int LPT, int VPL>
-__device__ __forceinline__ void walk(const GateParams &a, int r, int block, int blocks, Slots<LPT> &slots,
-                                     int32_t *count, Sums<VPL> &sum) {
-  constexpr int TPW = 32 / LPT;  // tokens per warp and step
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane & (LPT - 1), grp = lane / LPT, e0 = sub * VPL;
+// ---------------------------------------------------------------- the top k
+// By value and index, round by round: the lane's two best at hand, the row's
+// best by a maximum over its lanes and the lowest lane that holds it.  A lane
+// that has spent both looks through its values again.
+template <int LPT, int VPL>
+__device__ __forceinline__ void pick_exact(const float (&z)[VPL], int k, int e0, int grp, Slots<LPT> &slots) {
+  const int lane = threadIdx.x & 31;
   const uint32_t grp_mask = LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1u) << (grp * LPT);
-  const uint64_t step = (uint64_t)blocks * kWarps * TPW;
-  const char *rows = a.z[r];
-  const uint8_t *mask = a.mask[r];
-  int32_t *ids = a.ids[r];
-  float *weights = a.w[r];
-  const int k = a.k;
-  uint64_t t = ((uint64_t)block * kWarps + warp) * TPW + grp;
-  float next[VPL];
-  load_token<T, VPL>(a, rows, mask, t, e0, next);
-  for (; t - grp < a.tokens; t += step) {
-    const bool have = t < a.tokens;
-    float z[VPL], ex[VPL];
+  uint32_t sel = 0;
+  float b1 = -INFINITY, b2 = -INFINITY;
+  int j1 = 0, j2 = 0;
+  auto look = [&]() {  // the lower index first among equals
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) z[j] = next[j];
-    load_token<T, VPL>(a, rows, mask, t + step, e0, next);  // in flight while this one is worked on
-    // the lane's two best, the lower index first among equals
-    float b1 = choosable(z[0]), b2 = -INFINITY;
-    int j1 = 0, j2 = 0;
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) {
-      const float v = choosable(z[j]);
+    for (int j = 0; j < VPL; ++j) {
+      const float v = (sel >> j) & 1u ? -INFINITY : choosable(z[j]);
       const bool first = v > b1, second = v > b2;
       b2 = first ? b1 : second ? v : b2;
       j2 = first ? j1 : second ? j : j2;
       b1 = first ? v : b1;
       j1 = first ? j : j1;
     }
-    float best = row_max<LPT>(b1);
-    const float top = best;
+  };
+  look();
+  for (int i = 0; i < k; ++i) {
+    const float best = row_max<LPT>(b1);
+    const uint32_t who = __ballot_sync(0xffffffffu, b1 == best) & grp_mask;
+    const bool win = lane == __ffs(who) - 1;
+    if (win) {
+      slots.id[grp][i] = best > -INFINITY ? e0 + j1 : -1;
+      slots.z[grp][i] = best;
+      sel |= 1u << j1;
+      b1 = b2;
+      j1 = j2;
+      b2 = -INFINITY;
+    }
+    const bool spent = win && b1 == -INFINITY && i + 1 < k;
+    if (__any_sync(0xffffffffu, spent)) {
+      if (spent) look();
+    }
+  }
+}
+
+// With keys, for the long rows (16 and 32 lanes), where selects are what bounds
+// the kernel: a logit's bits as an ordered integer, the lowest 8 (9) replaced
+// by the index, lower indices larger.  Keys are all different, so the insertion
+// into a lane's three best is five minima and maxima, and a round is one
+// maximum over the lanes and three moves in the lane that has it.  slots.id
+// receives the k + 1 best keys.  Returns true where they may be wrong, and
+// pick_exact decides:
+//  - two fp32 logits that differ in the dropped bits alone (a relative 2^-15)
+//    come out in index order: two neighbours among the k + 1 best agree in all
+//    other bits (bf16 logits keep all their bits);
+//  - -0 comes below +0: a zero is among them;
+//  - a lane holds its three best: one that has spent them may have had more.
+// (The caller sees to rows with a NaN, whose keys are the largest.)
+// 131072 tokens x 256 experts, top 8, fp32: 120 us by pick_exact alone, 87 us
+// with keys (733 and 460 instructions per token; integer instructions bound
+// both, at 72% and 70% of the issue slots).
+constexpr uint32_t kFirstKey = 0x00800000u;  // of the lowest number; -inf lies below
+
+template <class T, int LPT, int VPL>
+__device__ __forceinline__ bool pick(const float (&z)[VPL], int k, int sub, int grp, Slots<LPT> &slots) {
+  constexpr uint32_t kIndex = LPT * VPL <= 256 ? 255u : 511u;
+  constexpr uint32_t kSame = std::is_same<T, F32>::value ? kIndex : 0;  // bf16: what is alike is equal
+  uint32_t k1 = 0, k2 = 0, k3 = 0;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const uint32_t u = __float_as_uint(z[j]);
+    const uint32_t ord = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    const uint32_t v = (ord & ~kIndex) | (uint32_t)(VPL - 1 - j);
+    const uint32_t m1 = min(k1, v), m2 = min(k2, m1);
+    k1 = max(k1, v);
+    k2 = max(k2, m1);
+    k3 = max(k3, m2);
+  }
+  // the lane's part of the index (kIndex - e0 - j, and e0 = sub * VPL)
+  const uint32_t part = kIndex - (uint32_t)(VPL - 1) - (uint32_t)sub * VPL;
+  k1 += part;
+  k2 += part;
+  k3 += part;
+  int32_t *out = slots.id[grp];
+#pragma unroll 4
+  for (int i = 0; i <= k; ++i) {
+    uint32_t best;
+    if constexpr (LPT == 32) {
+      best = __reduce_max_sync(0xffffffffu, k1);
+    } else {
+      best = k1;
+#pragma unroll
+      for (int d = LPT / 2; d > 0; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+    }
+    if (k1 == best) {  // one lane; or all of them, with nothing left (0)
+      out[i] = (int32_t)best;
+      k1 = k2;
+      k2 = k3;
+      k3 = 0;
+    }
+  }
+  __syncwarp();
+  bool doubt = k1 == 0;
+  if (sub < k) {
+    const uint32_t a = (uint32_t)out[sub], b = (uint32_t)out[sub + 1];
+    // (a pair below kFirstKey is two of -inf: equal, and not chosen)
+    doubt = doubt || (a >= kFirstKey && ((a ^ b) <= kSame || b - (0x7fffffffu - kIndex) <= 2 * kIndex + 1 ||
+                                         a - (0x7fffffffu - kIndex) <= 2 * kIndex + 1));
+  }
+  return doubt;
+}
+
+// The tokens of rank r that fall to this block.
+template <class T, int LPT, int VPL>
+__device__ __forceinline__ void walk(const GateParams &a, int r, int block, int blocks, Slots<LPT> &slots,
+                                     float *buf, int32_t *count, Sums<VPL> &sum) {
+  constexpr int TPW = 32 / LPT;  // tokens per warp and step
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane & (LPT - 1), grp = lane / LPT, e0 = sub * VPL;
+  const uint64_t step = (uint64_t)blocks * kWarps * TPW;
+  const char *rows = a.z[r];
+  const uint8_t *mask = a.mask[r];
+  int32_t *ids = a.ids[r];
+  float *weights = a.w[r];
+  const int k = a.k;
+  float *row_buf = buf + warp * 32 * VPL;
+  uint64_t t = ((uint64_t)block * kWarps + warp) * TPW + grp;
+  float next[VPL];
+  const char *row = rows + t * (uint64_t)a.E * T::kBytes;
+  const uint64_t row_step = step * (uint64_t)a.E * T::kBytes;
+  load_token<T, VPL>(a, row, mask, t, e0, next);
+  for (; t - grp < a.tokens; t += step) {
+    const bool have = t < a.tokens;
+    row += row_step;
+    float z[VPL], ex[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) z[j] = next[j];
+    load_token<T, VPL>(a, row, mask, t + step, e0, next);  // in flight while this one is worked on
+    float top = choosable(z[0]);
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) top = fmaxf(top, z[j]);
+    top = row_max<LPT>(top);
     bool live;
     const float total = row_exp<LPT, VPL>(z, top, ex, &live);
     const float inv = live ? reciprocal(total) : 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) sum.p[j] = fmaf(ex[j], inv, sum.p[j]);
     sum.tokens += (live && sub == 0) ? 1 : 0;
-    uint32_t sel = 0;
-    for (int i = 0; i < k; ++i) {
-      if (i > 0) best = row_max<LPT>(b1);
-      const uint32_t who = __ballot_sync(0xffffffffu, b1 == best) & grp_mask;
-      const bool win = lane == __ffs(who) - 1;
-      if (win) {
-        const bool found = best > -INFINITY;
-        slots.id[grp][i] = found ? e0 + j1 : -1;
-        slots.z[grp][i] = best;
-        if (found) atomicAdd(&count[e0 + j1], 1);  // integers: any order gives the same sum
-        sel |= 1u << j1;
-        b1 = b2;
-        j1 = j2;
-        b2 = -INFINITY;
-      }
-      // a lane that has spent both looks for its next best two
-      const bool spent = win && b1 == -INFINITY && i + 1 < k;
-      if (__any_sync(0xffffffffu, spent)) {
-        if (spent) {
+    bool exact = true;
+    if constexpr (LPT >= kMaxK) {
 #pragma unroll
-          for (int j = 0; j < VPL; ++j) {
-            const float v = (sel >> j) & 1u ? -INFINITY : choosable(z[j]);
-            const bool first = v > b1, second = v > b2;
-            b2 = first ? b1 : second ? v : b2;
-            j2 = first ? j1 : second ? j : j2;
-            b1 = first ? v : b1;
-            j1 = first ? j : j1;
-          }
-        }
-      }
+      for (int j = 0; j < VPL; j += 4)
+        *reinterpret_cast<float4 *>(&row_buf[lane * VPL + j]) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+      exact = __any_sync(0xffffffffu, pick<T, LPT, VPL>(z, k, sub, grp, slots) || isnan(total));
     }
+    if (exact) pick_exact<LPT, VPL>(z, k, e0, grp, slots);
     __syncwarp();
-    // slot i is lane i % LPT's: its weight, and the chosen weights' sum
-    float share = 1.0f;
-    if (a.norm) {
-      float s = 0.0f;
-      for (int i = sub; i < k; i += LPT)
-        if (slots.id[grp][i] >= 0) s += exp_diff(slots.z[grp][i], top);
-      share = row_sum<LPT>(s);
+    constexpr int kMine = LPT >= kMaxK ? 1 : LPT == 1 ? 8 : kMaxK / LPT;  // slots of a lane: sub, sub + LPT, ...
+    int id[kMine];
+    float w[kMine], share = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int i = sub + q * LPT;
+      id[q] = i < k ? slots.id[grp][i] : exact ? -1 : 0;
+      float v = 0.0f;
+      if (exact) {
+        v = i < k ? slots.z[grp][i] : 0.0f;
+      } else if constexpr (LPT >= kMaxK) {
+        constexpr int kIndex = LPT * VPL <= 256 ? 255 : 511;
+        id[q] = (uint32_t)id[q] >= kFirstKey ? kIndex - (id[q] & kIndex) : -1;
+        v = id[q] >= 0 ? row_buf[grp * LPT * VPL + id[q]] : 0.0f;
+      }
+      w[q] = id[q] >= 0 ? exp_diff(v, top) : 0.0f;
+      share += w[q];
+      if (id[q] >= 0) atomicAdd(&count[id[q]], 1);  // integers: any order gives the same sum
     }
-    const float per = a.norm ? reciprocal(share) : inv;
+    float per = inv;  // (carries the NaN of a row that holds one)
+    if (a.norm) {
+      share = row_sum<LPT>(share);
+      per = isnan(inv) ? inv : reciprocal(share);
+    }
     if (have) {
-      for (int i = sub; i < k; i += LPT) {
-        const int id = slots.id[grp][i];
-        ids[t * k + i] = id;
-        // (inv carries the NaN of a row that holds one)
-        weights[t * k + i] = id < 0 ? 0.0f : a.norm && !isnan(inv) ? exp_diff(slots.z[grp][i], top) * per
-                                                                  : exp_diff(slots.z[grp][i], top) * inv;
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        const int i = sub + q * LPT;
+        if (i < k) {
+          ids[t * k + i] = id[q];
+          weights[t * k + i] = id[q] < 0 ? 0.0f : w[q] * per;
+        }
       }
     }
     __syncwarp();
@@ -267,7 +362,7 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
 // probabilities goes to thread e % kNT's calls of `take(e, p)`, and the number
 // of tokens to every thread.  Ends with a barrier.
 template <int LPT, int VPL, class Take>
-__device__ __forceinline__ int32_t gather_block(Sums<VPL> &sum, float (&buf)[kWarps][LPT * VPL],
+__device__ __forceinline__ int32_t gather_block(Sums<VPL> &sum, float *buf,
                                                 int32_t (&tok)[kWarps], int E, Take take) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -277,16 +372,17 @@ __device__ __forceinline__ int32_t gather_block(Sums<VPL> &sum, float (&buf)[kWa
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum.tokens += __shfl_xor_sync(0xffffffffu, sum.tokens, d);
+  __syncthreads();  // the warps have done with their rows
   if (lane == 0) tok[warp] = sum.tokens;
   if (lane < LPT) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) buf[warp][lane * VPL + j] = sum.p[j];
+    for (int j = 0; j < VPL; ++j) buf[(warp * LPT + lane) * VPL + j] = sum.p[j];
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kNT) {
     float p = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) p += buf[w][e];
+    for (int w = 0; w < kWarps; ++w) p += buf[w * LPT * VPL + e];
     take(e, p);
   }
   int32_t tokens = 0;
@@ -307,15 +403,22 @@ __device__ __forceinline__ void clear(Sums<VPL> &sum, int32_t *count, int n) {
 
 __device__ __forceinline__ float warp_sum(float v) { return row_sum<32>(v); }
 
+// A block's buffer: the rows that its warps are at (long rows only, see pick),
+// then the warps' sums.
+template <int LPT, int VPL>
+constexpr int buf_floats() {
+  return kWarps * (LPT >= kMaxK ? 32 : LPT) * VPL;
+}
+
 template <class T, int LPT, int VPL>
 __global__ void __launch_bounds__(kNT) rc_gate_kernel(const __grid_constant__ GateParams a) {
-  __shared__ float buf[kWarps][LPT * VPL];
+  __shared__ __align__(16) float buf[buf_floats<LPT, VPL>()];
   __shared__ Slots<LPT> slots[kWarps];
   __shared__ int32_t tok[kWarps], count[LPT * VPL];
   Sums<VPL> sum;
   clear(sum, count, LPT * VPL);
   pdl_wait();
-  walk<T, LPT, VPL>(a, blockIdx.y, blockIdx.x, gridDim.x, slots[threadIdx.x >> 5], count, sum);
+  walk<T, LPT, VPL>(a, blockIdx.y, blockIdx.x, gridDim.x, slots[threadIdx.x >> 5], buf, count, sum);
   const uint64_t b = (uint64_t)blockIdx.y * gridDim.x + blockIdx.x;
   const int32_t tokens = gather_block<LPT>(sum, buf, tok, a.E, [&](int e, float p) {
     a.part[b * a.E + e] = make_float2(p, __int_as_float(count[e]));
@@ -326,7 +429,7 @@ __global__ void __launch_bounds__(kNT) rc_gate_kernel(const __grid_constant__ Ga
 // Few tokens: one block walks all ranks and finishes by itself.
 template <class T, int LPT, int VPL>
 __global__ void __launch_bounds__(kNT) rc_gate_one_kernel(const __grid_constant__ GateParams a) {
-  __shared__ float buf[kWarps][LPT * VPL];
+  __shared__ __align__(16) float buf[buf_floats<LPT, VPL>()];
   __shared__ Slots<LPT> slots[kWarps];
   __shared__ int32_t tok[kWarps], count[LPT * VPL];
   __shared__ float total_p[LPT * VPL], dots[kWarps];
@@ -336,7 +439,7 @@ __global__ void __launch_bounds__(kNT) rc_gate_one_kernel(const __grid_constant_
   for (int r = 0; r < a.p; ++r) {
     Sums<VPL> sum;
     clear(sum, count, LPT * VPL);
-    walk<T, LPT, VPL>(a, r, 0, 1, slots[threadIdx.x >> 5], count, sum);
+    walk<T, LPT, VPL>(a, r, 0, 1, slots[threadIdx.x >> 5], buf, count, sum);
     m += gather_block<LPT>(sum, buf, tok, a.E, [&](int e, float p) {  // thread e % kNT only
       const int32_t c = count[e];
       a.counts[r][e] = c;
@@ -475,9 +578,13 @@ __global__ void __launch_bounds__(kBackNT) rc_gate_backward_kernel(const __grid_
   const int k = a.k;
   uint64_t t = ((uint64_t)blockIdx.x * kBackWarps + warp) * TPW + grp;
   float next[VPL];
-  load_token<T, VPL>(a, rows, mask, t, e0, next);
+  const char *row = rows + t * (uint64_t)a.E * T::kBytes;
+  const uint64_t row_step = step * (uint64_t)a.E * T::kBytes;
+  load_token<T, VPL>(a, row, mask, t, e0, next);
   for (; t - grp < a.tokens; t += step) {
     const bool have = t < a.tokens;
+    char *out = dz + (row - rows);
+    row += row_step;
     float z[VPL], p[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) z[j] = next[j];
@@ -488,7 +595,7 @@ __global__ void __launch_bounds__(kBackNT) rc_gate_backward_kernel(const __grid_
         if (id >= 0 && id < a.E) row_grad[id] = __float_as_uint(dw[t * k + i]);
       }
     }
-    load_token<T, VPL>(a, rows, mask, t + step, e0, next);  // in flight while this one is worked on
+    load_token<T, VPL>(a, row, mask, t + step, e0, next);  // in flight while this one is worked on
     float top = choosable(z[0]);
 #pragma unroll
     for (int j = 1; j < VPL; ++j) top = fmaxf(top, z[j]);
@@ -537,7 +644,6 @@ __global__ void __launch_bounds__(kBackNT) rc_gate_backward_kernel(const __grid_
       }
     }
     if (!have) continue;
-    char *out = dz + t * (uint64_t)a.E * T::kBytes;
     if (a.vec) {
 #pragma unroll
       for (int j = 0; j < VPL; j += V) {

@@ -121,6 +121,10 @@ def test_many_tokens_per_block(rc):
     x = z[0].double()
     first = torch.sort(-x, dim=1, stable=True).indices[:, :2]
     assert torch.equal(g.ids[0].long(), first)
+    z32 = make(1, 30000, 64, "f32", seed=5)
+    h = Gate(rc, z32, 6)
+    torch.cuda.synchronize()
+    assert torch.equal(h.ids[0].long(), torch.sort(-z32[0].double(), dim=1, stable=True).indices[:, :6])
     assert torch.equal(g.counts[0].long(), torch.bincount(first.reshape(-1), minlength=16))
     mean = torch.softmax(x, 1).mean(0)
     assert float((g.stats[16:32].double() - mean).abs().max()) <= (40000 + 64) * U * float(mean.max())
@@ -138,6 +142,24 @@ def test_ties_go_to_the_lowest_index(rc, dt):
     g = Gate(rc, z, 5, norm=False)
     torch.cuda.synchronize()
     check_forward(g, reference(z, 5, None, False, 0.02), z, 24)
+
+
+@pytest.mark.parametrize("e,k", [(8, 3), (64, 8), (200, 8), (256, 16), (512, 16)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_neighbours_that_differ_in_the_last_bits(rc, e, k, sign):
+    """fp32 logits a few units of the last place apart, in every order, and the like at the k-th place."""
+    t = 64
+    gen = torch.Generator(device="cuda").manual_seed(e)
+    step = torch.randint(0, 5, (t, e), generator=gen, device="cuda")
+    z = (sign * (1.5 + step.double() * 2.0 ** -23)).float()
+    z[t // 2:] = torch.randn(t - t // 2, e, generator=gen, device="cuda")
+    last = torch.sort(z, dim=1, descending=True).values[:, k - 1]
+    for i in range(t // 2, t):                     # a rival one unit above, below or at the k-th largest
+        j = int(torch.randint(0, e, (1,), generator=gen, device="cuda"))
+        z[i, j] = torch.nextafter(last[i], last[i] + (i % 3 - 1) * 10.0) if i % 3 != 1 else last[i]
+    g = Gate(rc, [z], k)
+    torch.cuda.synchronize()
+    check_forward(g, reference([z], k, None, True, 0.02), [z], e)
 
 
 @pytest.mark.parametrize("kind", ["some", "one_rank", "all"])
