@@ -1289,6 +1289,7 @@ rc_status rc_finalize(void) {
   }
   cudaSetDevice(cur);
   noalloc_scratch_forget();
+  ce_forget();
   return st;
 }
 

@@ -181,6 +181,7 @@ size_t ce_workspace(const CeJob &j);
 cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s);
 cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s);
 cudaError_t read_and_clear_ce_timeouts(unsigned int *count);
+void ce_forget();  // drop what is known of the devices (rc_finalize)
 cudaError_t launch_reduce(const ReduceJob &job, cudaStream_t s);
 bool fold_tma_eligible(const FoldJob &job);
 cudaError_t launch_fold_tma(const FoldJob &job, cudaStream_t s);

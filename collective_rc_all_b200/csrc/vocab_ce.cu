@@ -18,11 +18,14 @@
 // it to the two products dW_r = G^T h (complete for the piece) and dh += G W
 // (fp32 sums in the workspace, rounded once at the end).
 //
-// Rounding G to bf16 (2^-9 relative at most on average, independent from
-// entry to entry) adds about as much error as the gradients' own rounding to
-// bf16.  With few tokens one entry, the target's, carries a row's whole
-// gradient and its rounding would show in every output of the row; there G is
-// kept as the sum of two bf16 planes (2^-17).
+// What is kept as bf16 is G / s, s the largest |dloss| of the tokens that
+// count, and the products are multiplied by s as they leave: with one weight
+// for all tokens (a mean) the target's entry, p - 1, is then near -1 and nearly
+// exact, where dloss itself would put its own rounding, the same for every
+// token, on all gradients.  The other entries' roundings (2^-9 relative at most
+// on average) are independent and add about as much as the gradients' own
+// rounding to bf16.  With few tokens one entry can carry a row's whole
+// gradient; there G / s is kept as the sum of two bf16 planes (2^-17).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -95,6 +98,7 @@ struct alignas(64) CeParams {
   char *dw[kMaxRanks];        // kBack without dw_tma
   const int32_t *target;
   const float *lse_in, *dloss;  // kGrad
+  float *scale;               // s: written by the first kGrad, read by the others and kBack
   float2 *part;               // kStats: [tile][N]
   float *ztarget;             // kStats: [N]
   const char *copy_from;      // kGrad: h to copy to copy_to, its ignored rows as zeros (or NULL)
@@ -210,6 +214,23 @@ __device__ __forceinline__ void dh_row(const CeParams &a, int kk, int *r, int *r
   *left = per - in;
 }
 
+// s, from the dloss of the tokens that count (finite ones; 1 if all are zero),
+// by the epilogue warps of every block.
+__device__ __forceinline__ float largest_dloss(const CeParams &a, float (&buf)[kEpiWarps]) {
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < a.N; i += kEpiWarps * 32) {
+    const float g = fabsf(a.dloss[i]);
+    if (a.target[i] != a.ignore && g < INFINITY) m = fmaxf(m, g);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = m;
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+#pragma unroll
+  for (int w = 0; w < kEpiWarps; ++w) m = fmaxf(m, buf[w]);
+  return m > 0.0f ? m : 1.0f;
+}
+
 // h for the product with G, by the epilogue warps while they wait for the
 // first tile: what ignored rows hold must not meet their zeros in G (NaN * 0).
 __device__ __forceinline__ void copy_hidden(const CeParams &a) {
@@ -234,6 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
   __shared__ uint32_t dead_s;
   __shared__ float2 join[MODE == kStats ? 4 : 1][kHalf];
   __shared__ uint64_t joined[4], join_free[4];  // kStats, per 32 rows
+  __shared__ float max_buf[MODE == kGrad ? kEpiWarps : 1];
   const uint32_t smem0 = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t c = cluster_rank();
@@ -407,7 +429,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     const uint32_t src0 = tmem + quarter * 64 + ((uint32_t)(quad * 32) << 16);
     const uint32_t box = smem0 + S * kStageBytes + warp * kBoxBytes;
     const uint32_t acc_empty_addr = first_block_addr(&acc_empty[0]);
-    if (MODE == kGrad && a.copy_from != nullptr) copy_hidden(a);
+    float scale = 1.0f;
+    if constexpr (MODE == kGrad) {
+      if (a.j0 == 0) {
+        scale = largest_dloss(a, max_buf);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = scale;
+      } else {
+        scale = *a.scale;
+      }
+      if (a.copy_from != nullptr) copy_hidden(a);
+    } else if constexpr (MODE == kBack) {
+      scale = *a.scale;
+    }
     uint32_t i = 0, nth = 0;
     bool ok = true;
     Tile w;
@@ -428,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         ycol = (live && y != a.ignore && y >= 0 && yt >= 0 && yt < min(cols, 64)) ? yt : -1;
         if constexpr (MODE == kGrad) {
           lse2 = live ? a.lse_in[row] * kLog2e : 0.0f;
-          g = live ? a.dloss[row] : 0.0f;
+          g = live ? a.dloss[row] / scale : 0.0f;
           // a label that is no word and not the ignored one poisons its row
           if (y < 0 || y >= a.V) g = __int_as_float(0x7fc00000);
           zero = !live || y == a.ignore;
@@ -543,6 +576,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         }
       } else if (w.dw || a.direct) {
         // bf16 rows of dW_r or of dh
+#pragma unroll
+        for (int q = 0; q < 64; ++q) z[q] *= scale;
         const int x0 = w.n * kBN + quarter * 64;
         int r = 0, v0 = row0, rows = a.N;
         if (w.dw) {
@@ -860,11 +895,12 @@ __global__ void __launch_bounds__(kThreads, 2) rc_ce_few_kernel(const __grid_con
   }
 }
 
-// dh = bf16(sum of the splits' sums, in order).  A thread has 8 columns of a
+// dh = bf16(s * sum of the splits' sums, in order).  A thread has 8 columns of a
 // row (dpad is a multiple of 8); `vec`: dh's rows are 16-byte multiples.
-__global__ void __launch_bounds__(kThreads) rc_ce_finish_kernel(const float *sums, char *dh, int64_t N, int D, int dpad,
-                                                                int splits, bool vec) {
+__global__ void __launch_bounds__(kThreads) rc_ce_finish_kernel(const float *sums, const float *scale, char *dh, int64_t N,
+                                                                int D, int dpad, int splits, bool vec) {
   pdl_wait();
+  const float sc = *scale;
   const int per = dpad / 8;
   const int64_t n = N * per;
   for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (int64_t)gridDim.x * kThreads) {
@@ -879,6 +915,8 @@ __global__ void __launch_bounds__(kThreads) rc_ce_finish_kernel(const float *sum
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = s == 0 ? p[e] : v[e] + p[e];
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= sc;
     if (vec) {
       store_vec<BF16, 8>(dh + (row * D + x) * 2, v);
     } else {
@@ -934,7 +972,7 @@ struct Plan {
   int planes, per_piece, pieces;  // of the gradients' pass
   int splits, kper, slots;        // of dh's k; sums kept (one or two per split)
   bool stacked;
-  size_t off_part, off_zt, off_h, off_w, off_g, off_dh, bytes;
+  size_t off_part, off_zt, off_h, off_w, off_g, off_dh, off_scale, bytes;
 };
 
 Plan make_plan(const CeShape &s, bool backward, bool copies) {
@@ -992,10 +1030,14 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
     q.slots = q.splits * (q.stacked ? 2 : 1);
     q.off_g = take((size_t)q.planes * N * q.per_piece * kBN * 2);
     q.off_dh = take((size_t)q.slots * N * q.dpad * 4);
+    q.off_scale = take(4);
   }
   q.bytes = at;
   return q;
 }
+
+// Devices on which each tile kernel has been allowed its shared memory.
+std::atomic<uint64_t> g_smem_ready[3];
 
 bool shape_of(Shape *q, int64_t mt, int64_t nt, int64_t nk, int64_t kper) {
   q->mt = (int)mt;
@@ -1009,7 +1051,7 @@ bool shape_of(Shape *q, int64_t mt, int64_t nt, int64_t nk, int64_t kper) {
 
 template <int MODE>
 cudaError_t gemm(CeParams &a, cudaStream_t s) {
-  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
+  std::atomic<uint64_t> &ready = g_smem_ready[MODE];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -1173,6 +1215,7 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
   z.target = j.target;
   z.lse_in = j.lse_in;
   z.dloss = j.dloss;
+  z.scale = reinterpret_cast<float *>(ws + q.off_scale);
   z.N = (int)N;
   z.D = D;
   z.C = q.C;
@@ -1218,7 +1261,11 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
   if (w.direct) return cudaSuccess;
   const int64_t grid = std::min<int64_t>(cdiv(N * (q.dpad / 8), kThreads), (int64_t)device_sm_count() * 8);
   return launch_kernel(rc_ce_finish_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, (const float *)sums,
-                       static_cast<char *>(j.dhidden), N, D, q.dpad, q.slots, dh_aligned);
+                       (const float *)z.scale, static_cast<char *>(j.dhidden), N, D, q.dpad, q.slots, dh_aligned);
+}
+
+void ce_forget() {
+  for (auto &m : g_smem_ready) m.store(0, std::memory_order_relaxed);
 }
 
 cudaError_t read_and_clear_ce_timeouts(unsigned int *count) {

@@ -464,7 +464,8 @@ rc_status rc_vocab_ce_forward(const void *hidden, const void *const *weight, con
  *   G_iv = dloss_i * (exp(z_iv - lse_i) - [v == target_i])   (0 if ignored)
  *   dhidden = sum over the ranks of G_r W_r,   dweight[r] = G_r^T hidden
  * dhidden [tokens][d] and dweight[r] [rows][d] bf16 are written, not added
- * to.  What an ignored token's hidden row holds (NaN too) does not reach
+ * to.  G is kept as bf16 shares of the largest |dloss| (two terms of it up to
+ * 128 tokens), so a weight below 2^-120 of the largest loses precision.  What an ignored token's hidden row holds (NaN too) does not reach
  * dweight; its dhidden row is zero.  A target outside [0, vocab) that is not
  * ignore_index makes the gradients NaN.  tokens 0 sets dweight to zero.
  */

@@ -258,6 +258,63 @@ def test_gradients_against_differences(rc):
         assert abs(fd - got) <= 2 * HALF * room + 1e-7
 
 
+@pytest.mark.parametrize("weight", [2.0 ** -11 * (1 + 2.0 ** -8), 1 / 1946, 3e-30, 1e20])
+def test_one_weight_for_all_tokens_is_not_rounded(rc, weight):
+    """dloss = weight everywhere: with p small, what is left of the error is the
+    results' own rounding, whose root mean square is at most half a step over
+    sqrt(3).  (2^-11 (1 + 2^-8) lies in the middle of two bf16 values.)"""
+    c = Case(512, 256, 6000, 2, seed=12, ignored=0.1, boost=0.0)
+    c.dloss.fill_(weight)
+    c.dloss[c.y == c.ignore] = float("nan")       # not among the tokens that count
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    h, w = c.h.double(), torch.cat([x.double() for x in c.w])
+    live = c.y != c.ignore
+    G = torch.softmax(h @ w.T, 1)
+    G[live, c.y[live].long()] -= 1
+    G *= torch.where(live, weight, 0.0)[:, None]
+    got = torch.cat([x.double() for x in c.dw])
+    for a, b in ((c.dh.double(), G @ w), (got, G.T @ h)):
+        assert float((a - b).norm()) <= 1.02 * HALF / 3 ** 0.5 * float(b.norm())
+
+
+@pytest.mark.parametrize("tokens", [30, 200])
+def test_weights_of_every_size(rc, tokens):
+    """dloss over forty orders of magnitude, zeros, signs; an infinite one stays in its row and in dweight."""
+    a, b = Case(tokens, 64, 500, 2, seed=13, ignored=0.0), Case(tokens, 64, 500, 2, seed=13, ignored=0.0)
+    for c in (a, b):
+        c.dloss.copy_(10.0 ** torch.linspace(-20, 18, tokens, device="cuda") * torch.where(torch.arange(tokens, device="cuda") % 2 == 0, 1.0, -1.0))
+        c.dloss[::7] = 0.0
+    b.dloss[3] = math.inf
+    for c in (a, b):
+        c.forward(rc)
+        c.backward(rc)
+    rc.rc_stream_status()
+    rows = torch.arange(tokens, device="cuda") != 3
+    assert bool((a.dh[::7] == 0).all()) and bool(torch.isfinite(a.dh).all()) and bool(torch.isfinite(b.dh[rows]).all())
+    assert torch.equal(a.dh[rows], b.dh[rows])
+    z = a.h.double() @ torch.cat([x.double() for x in a.w]).T
+    G = torch.softmax(z, 1)
+    G[torch.arange(tokens, device="cuda"), a.y.long()] -= 1
+    dh = G * a.dloss.double()[:, None] @ torch.cat([x.double() for x in a.w])
+    # row by row: two roundings to bf16 of entries that are independent.  G is kept as a share of the largest weight s,
+    # and bf16 has no normal value below 2^-126: an entry that is smaller is off by 2^-126 at most, so a row by at
+    # most s * 2^-126 * sum_v |W_v| (the rows whose weight is 10^-38 of s).
+    err, size = (a.dh.double() - dh).norm(dim=1), dh.norm(dim=1)
+    least = float(a.dloss.abs().max()) * 2.0 ** -126 * float(torch.cat([x.double() for x in a.w]).abs().sum(0).norm())
+    assert bool((err <= 2.0 ** -7 * size + least).all())
+
+
+def test_zero_weights(rc):
+    c = Case(150, 64, 500, 2, seed=14)
+    c.dloss.zero_()
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    assert bool((c.dh == 0).all()) and all(bool((x == 0).all()) for x in c.dw)
+
+
 def test_runs_repeat_bit_for_bit(rc):
     a, b = Case(700, 192, 3001, 4, seed=7), Case(700, 192, 3001, 4, seed=7)
     for c in (a, b):
