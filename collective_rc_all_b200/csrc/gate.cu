@@ -39,6 +39,7 @@ constexpr int kWarps = kNT / 32;
 constexpr int kBackNT = 256;
 constexpr int kMaxK = 16;
 constexpr int kStatBlocks = 8;  // the cluster of rc_gate_stats_kernel
+constexpr int kStatNT = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct GateParams {
@@ -466,27 +467,28 @@ __global__ void __launch_bounds__(kNT) rc_gate_one_kernel(const __grid_constant_
   }
 }
 
-// Adds the blocks' partials in block order.  A cluster of kStatBlocks blocks,
-// each `span` neighbouring experts (a power of two); within a block, 256 /
-// span groups of threads share the partials.
-__global__ void __cluster_dims__(kStatBlocks, 1, 1) __launch_bounds__(256)
+// Adds the blocks' partials in a fixed order.  A cluster of kStatBlocks blocks,
+// each `span` neighbouring experts (a power of two, 64 at most); within a
+// block, kStatNT / span groups of threads share the partials, kIn loads of
+// each in flight.
+__global__ void __cluster_dims__(kStatBlocks, 1, 1) __launch_bounds__(kStatNT)
     rc_gate_stats_kernel(const __grid_constant__ GateParams a, int span) {
-  __shared__ float sp[256];
+  constexpr int kIn = 4, kStatWarps = kStatNT / 32;
+  __shared__ float sp[kStatWarps][64];
   __shared__ int32_t sc[kMaxRanks][64];
-  __shared__ int64_t tot[8];
-  __shared__ float red[8], dots[kStatBlocks];
+  __shared__ int64_t tot[kStatWarps];
+  __shared__ float red[2], dots[kStatBlocks];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = threadIdx.x & (span - 1), g = threadIdx.x / span, groups = 256 / span;
+  const int col = threadIdx.x & (span - 1), g = threadIdx.x / span, groups = kStatNT / span;
   const int e = blockIdx.x * span + col;
-  for (int i = threadIdx.x; i < kMaxRanks * 64; i += 256) sc[i / 64][i % 64] = 0;
+  for (int i = threadIdx.x; i < kMaxRanks * 64; i += kStatNT) sc[i / 64][i % 64] = 0;
   __syncthreads();
   pdl_wait();
+  const int rows = a.p * a.blocks;
   int64_t m = 0;
-  for (int b = threadIdx.x; b < a.p * a.blocks; b += 256) m += a.part_m[b];
+  for (int b = threadIdx.x; b < rows; b += kStatNT) m += a.part_m[b];
   float s = 0.0f;
   if (e < a.E) {
-    constexpr int kIn = 8;  // loads in flight
-    const int rows = a.p * a.blocks;
     for (int b0 = g; b0 < rows; b0 += kIn * groups) {
       float2 v[kIn];
 #pragma unroll
@@ -502,40 +504,48 @@ __global__ void __cluster_dims__(kStatBlocks, 1, 1) __launch_bounds__(256)
       }
     }
   }
-  sp[threadIdx.x] = s;
+  // the groups of a warp (those of span 64 take two warps each), then the warps
+  for (int d = 16; d >= span; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane < span) sp[warp][col] = s;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m += __shfl_xor_sync(0xffffffffu, m, d);
   if (lane == 0) tot[warp] = m;
   __syncthreads();
-  m = 0;
+  float dot = 0.0f, M = 0.0f;
+  if (threadIdx.x < 64) {
+    m = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m += tot[w];
-  const float M = (float)m, per = fmaxf(M, 1.0f);
-  float dot = 0.0f;
-  if (g == 0 && e < a.E) {
-    s = 0.0f;
-    for (int q = 0; q < groups; ++q) s += sp[q * span + col];
-    int64_t c = 0;
-    for (int r = 0; r < a.p; ++r) {
-      a.counts[r][e] = sc[r][col];
-      c += sc[r][col];
+    for (int w = 0; w < kStatWarps; ++w) m += tot[w];
+    M = (float)m;
+    const float per = fmaxf(M, 1.0f);
+    if (threadIdx.x < span && e < a.E) {
+      s = 0.0f;
+      if (span < 64) {
+#pragma unroll
+        for (int w = 0; w < kStatWarps; ++w) s += sp[w][col];
+      } else {
+#pragma unroll
+        for (int w = 0; w < kStatWarps; w += 2) s += sp[w + warp][col];
+      }
+      int64_t c = 0;
+      for (int r = 0; r < a.p; ++r) {
+        a.counts[r][e] = sc[r][col];
+        c += sc[r][col];
+      }
+      const float f = (float)c / ((float)a.k * per), mean = s / per;
+      a.stats[e] = f;
+      a.stats[a.E + e] = mean;
+      dot = f * mean;
     }
-    const float f = (float)c / ((float)a.k * per), mean = s / per;
-    a.stats[e] = f;
-    a.stats[a.E + e] = mean;
-    dot = f * mean;
+    dot = warp_sum(dot);
+    if (lane == 0) red[warp] = dot;
   }
-  dot = warp_sum(dot);
-  if (lane == 0) red[warp] = dot;
   __syncthreads();
   if (threadIdx.x == 0) {
-    dot = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) dot += red[w];
     // into the first block's shared memory
     uint32_t there;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(smem_addr(&dots[blockIdx.x])));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(dot) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(red[0] + red[1]) : "memory");
   }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -685,7 +695,7 @@ cudaError_t run(const GateJob &job, GateParams &a, cudaStream_t s) {
     return err;
   int span = 1;
   while (span * kStatBlocks < job.experts) span *= 2;
-  return launch_kernel(rc_gate_stats_kernel, dim3(kStatBlocks), dim3(256), 0, s, a, span);
+  return launch_kernel(rc_gate_stats_kernel, dim3(kStatBlocks), dim3(kStatNT), 0, s, a, span);
 }
 
 // Lanes per token: the fewest that hold the row at 8 values each, so that

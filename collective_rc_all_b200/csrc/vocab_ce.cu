@@ -244,6 +244,15 @@ __device__ __forceinline__ void copy_hidden(const CeParams &a) {
   }
 }
 
+// The warp has read its part of an accumulator.  (Released, not relaxed: handed
+// over any earlier, the products of dh and dW crowd the copies out: 100 x 4096 x
+// 32000 281 -> 298 us.)
+__device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
+  tc_fence_before_sync();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_cluster(bar);
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
     rc_ce_gemm_kernel(const __grid_constant__ CeParams a) {
@@ -467,9 +476,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           zero = !live || y == a.ignore;
         }
       }
+      if constexpr (!LOGITS) {
+        const uint32_t acc = i & 1, src = src0 + acc * kBN;
+        if (!__all_sync(0xffffffffu, flow.wait(&acc_full[acc], (i / 2) & 1))) break;
+        ++i;
+        tc_fence_after_sync();
+        const int x0 = w.n * kBN + quarter * 64;
+        // 16 columns at a time, straight into the staging rows: 60 registers where
+        // the whole tile in registers takes 95, and 2% of dh and dW's time
+        if (w.dw || a.direct) {  // bf16 rows of dW_r or of dh
+          int r = 0, v0 = row0, rows = a.N;
+          if (w.dw) {
+            const int j = a.j0 + w.m;
+            r = j / a.tpr;
+            v0 = (j - r * a.tpr) * kBN + (int)c * kHalf + quad * 32;
+            rows = a.rows[r];
+          }
+          staging_free(lane);
+#pragma unroll 1
+          for (int q = 0; q < 64; q += 16) {
+            float v[16];
+            tmem_load16(src + q, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= scale;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              sts128(staging_unit(box, lane, (q + e) / 8),
+                     make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                                pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7])));
+          }
+          hand_over(acc_empty_addr + acc * 8, lane);
+          staging_ready();
+          if (!w.dw || a.dw_tma) {
+            if (lane == 0 && v0 < rows && x0 < a.D) {
+              tma_store_2d(w.dw ? &a.out[r] : &a.dh, x0, v0, box);
+              bulk_commit();
+            }
+          } else {  // rows of any length and base: a warp's stores are neighbours
+            const int n = min(32, rows - v0);
+            for (int e = 0; e < n; ++e) {
+              uint16_t *out = reinterpret_cast<uint16_t *>(a.dw[r]) + (int64_t)(v0 + e) * a.D;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int x = h * 32 + lane;
+                uint16_t v;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(staging_unit(box, e, x / 8) + (x & 7) * 2));
+                if (x0 + x < a.D) out[x0 + x] = v;
+              }
+            }
+            __syncwarp();
+          }
+        } else {  // fp32 sums of dh
+          const int y0 = a.stacked ? quad * 32 : row0, slot = a.stacked ? w.s * 2 + (int)c : w.s;
+#pragma unroll 1
+          for (int h = 0; h < 64; h += 32) {
+            staging_free(lane);
+#pragma unroll 1
+            for (int q = 0; q < 32; q += 16) {
+              float v[16];
+              tmem_load16(src + h + q, v);
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                sts128(staging_unit(box, lane, (q + e) / 4),
+                       make_uint4(__float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
+                                  __float_as_uint(v[e + 3])));
+            }
+            staging_ready();
+            // one add per element and launch, launches in stream order: a fixed order
+            if (lane == 0 && y0 < a.N && x0 + h < a.D) {
+              if (a.first) tma_store_3d(&a.dh, x0 + h, y0, slot, box);
+              else tma_add_3d(&a.dh, x0 + h, y0, slot, box);
+              bulk_commit();
+            }
+          }
+          hand_over(acc_empty_addr + acc * 8, lane);
+        }
+      } else {
       // the tile, or its first chunk; then the other chunks are added
       float z[64];
-      const int nc = LOGITS ? (a.main.nk + a.chunk - 1) / a.chunk : 1;
+      const int nc = (a.main.nk + a.chunk - 1) / a.chunk;
       for (int u = 0; u < nc; ++u, ++i) {
         const uint32_t acc = i & 1;
         if (!__all_sync(0xffffffffu, flow.wait(&acc_full[acc], (i / 2) & 1))) {
@@ -490,17 +575,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
-          // relaxed hands the accumulators over 0.3 us earlier, which short
-          // sums need (logits of 4000 x 256 x 10000: 35 -> 29 us); for dh and
-          // dW it only makes the products crowd the copies out (100 x 4096 x
-          // 32000: 281 -> 298 us)
-          if (LOGITS) mbar_arrive_cluster_relaxed(acc_empty_addr + acc * 8);
-          else mbar_arrive_cluster(acc_empty_addr + acc * 8);
-        }
+        // relaxed: 0.3 us earlier, which short sums need (logits of 4000 x 256 x
+        // 10000: 35 -> 29 us)
+        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_addr + acc * 8);
       }
       if (!ok) break;
-      if constexpr (LOGITS) {
         if (cols < 64) {
 #pragma unroll
           for (int q = 0; q < 64; ++q) z[q] = q < cols ? z[q] : -INFINITY;
@@ -572,63 +651,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
               tma_store_3d(&a.out[0], w.n * kBN + quarter * 64, row0, plane, box);
               bulk_commit();
             }
-          }
-        }
-      } else if (w.dw || a.direct) {
-        // bf16 rows of dW_r or of dh
-#pragma unroll
-        for (int q = 0; q < 64; ++q) z[q] *= scale;
-        const int x0 = w.n * kBN + quarter * 64;
-        int r = 0, v0 = row0, rows = a.N;
-        if (w.dw) {
-          const int j = a.j0 + w.m;
-          r = j / a.tpr;
-          v0 = (j - r * a.tpr) * kBN + (int)c * kHalf + quad * 32;
-          rows = a.rows[r];
-        }
-        staging_free(lane);
-#pragma unroll
-        for (int q = 0; q < 64; q += 8)
-          sts128(staging_unit(box, lane, q / 8),
-                 make_uint4(pack_bf16x2(z[q], z[q + 1]), pack_bf16x2(z[q + 2], z[q + 3]),
-                            pack_bf16x2(z[q + 4], z[q + 5]), pack_bf16x2(z[q + 6], z[q + 7])));
-        staging_ready();
-        if (!w.dw || a.dw_tma) {
-          if (lane == 0 && v0 < rows && x0 < a.D) {
-            tma_store_2d(w.dw ? &a.out[r] : &a.dh, x0, v0, box);
-            bulk_commit();
-          }
-        } else {  // rows of any length and base: a warp's stores are neighbours
-          const int n = min(32, rows - v0);
-          for (int e = 0; e < n; ++e) {
-            uint16_t *out = reinterpret_cast<uint16_t *>(a.dw[r]) + (int64_t)(v0 + e) * a.D;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int x = h * 32 + lane;
-              uint16_t v;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(staging_unit(box, e, x / 8) + (x & 7) * 2));
-              if (x0 + x < a.D) out[x0 + x] = v;
-            }
-          }
-          __syncwarp();
-        }
-      } else {
-        const int x0 = w.n * kBN + quarter * 64;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          staging_free(lane);
-#pragma unroll
-          for (int q = 0; q < 32; q += 4)
-            sts128(staging_unit(box, lane, q / 4),
-                   make_uint4(__float_as_uint(z[h * 32 + q]), __float_as_uint(z[h * 32 + q + 1]),
-                              __float_as_uint(z[h * 32 + q + 2]), __float_as_uint(z[h * 32 + q + 3])));
-          staging_ready();
-          // one add per element and launch, launches in stream order: a fixed order
-          const int y0 = a.stacked ? quad * 32 : row0, slot = a.stacked ? w.s * 2 + (int)c : w.s;
-          if (lane == 0 && y0 < a.N && x0 + h * 32 < a.D) {
-            if (a.first) tma_store_3d(&a.dh, x0 + h * 32, y0, slot, box);
-            else tma_add_3d(&a.dh, x0 + h * 32, y0, slot, box);
-            bulk_commit();
           }
         }
       }
