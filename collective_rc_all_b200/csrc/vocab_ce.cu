@@ -13,8 +13,8 @@
 //
 // Everything of size N V D is a bf16 tensor-core product with fp32
 // accumulators; the logits live in tensor memory only.  The gradients'
-// pass goes over the vocabulary in pieces of a few thousand columns: it
-// computes the piece's logits again, writes G for the piece as bf16, and feeds
+// pass goes over the vocabulary in pieces (as many columns as keep G below
+// 128 MiB): it computes the piece's logits again, writes G for the piece as bf16, and feeds
 // it to the two products dW_r = G^T h (complete for the piece) and dh += G W
 // (fp32 sums in the workspace, rounded once at the end).
 //
@@ -552,107 +552,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           hand_over(acc_empty_addr + acc * 8, lane);
         }
       } else {
-      // the tile, or its first chunk; then the other chunks are added
-      float z[64];
-      const int nc = (a.main.nk + a.chunk - 1) / a.chunk;
-      for (int u = 0; u < nc; ++u, ++i) {
-        const uint32_t acc = i & 1;
-        if (!__all_sync(0xffffffffu, flow.wait(&acc_full[acc], (i / 2) & 1))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        if (u == 0) {
-          tmem_load64(src0 + acc * kBN, z);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 64; q += 16) {
-            float v[16];
-            tmem_load16(src0 + acc * kBN + q, v);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) z[q + e] += v[e];
-          }
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        // relaxed: 0.3 us earlier, which short sums need (logits of 4000 x 256 x
-        // 10000: 35 -> 29 us)
-        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_addr + acc * 8);
-      }
-      if (!ok) break;
-        if (cols < 64) {
-#pragma unroll
-          for (int q = 0; q < 64; ++q) z[q] = q < cols ? z[q] : -INFINITY;
-        }
-        if constexpr (MODE == kStats) {
-          if (ycol >= 0) {
-            float zt = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 64; ++q) zt = ycol == q ? z[q] : zt;
-            a.ztarget[row] = zt;
-          }
-          float mq[4] = {z[0], z[1], z[2], z[3]};  // four chains each: short waits
-#pragma unroll
-          for (int q = 4; q < 64; ++q) mq[q & 3] = fmaxf(mq[q & 3], z[q]);
-          const float m = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-          const float base = m > -INFINITY ? m * kLog2e : 0.0f;
-          float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int q = 0; q < 64; ++q) sq[q & 3] += ex2(fmaf(z[q], kLog2e, -base));
-          // the four warps of these rows; the first one writes the tile's pair
-          if (quarter != 0 && nth > 0 &&
-              !__all_sync(0xffffffffu, flow.wait(&join_free[quad], (nth - 1) & 1)))
+        // the tile, or its first chunk; then the other chunks are added
+        float z[64];
+        const int nc = (a.main.nk + a.chunk - 1) / a.chunk;
+        for (int u = 0; u < nc; ++u, ++i) {
+          const uint32_t acc = i & 1;
+          if (!__all_sync(0xffffffffu, flow.wait(&acc_full[acc], (i / 2) & 1))) {
+            ok = false;
             break;
-          join[quarter][row_l] = make_float2(m, (sq[0] + sq[1]) + (sq[2] + sq[3]));
+          }
+          tc_fence_after_sync();
+          if (u == 0) {
+            tmem_load64(src0 + acc * kBN, z);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 64; q += 16) {
+              float v[16];
+              tmem_load16(src0 + acc * kBN + q, v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) z[q + e] += v[e];
+            }
+          }
+          tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&joined[quad]);
-          if (quarter == 0) {
-            if (!__all_sync(0xffffffffu, flow.wait(&joined[quad], nth & 1))) break;
-            float2 v[4];
+          // relaxed: 0.3 us earlier, which short sums need (logits of 4000 x 256 x
+          // 10000: 35 -> 29 us)
+          if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_addr + acc * 8);
+        }
+        if (!ok) break;
+          if (cols < 64) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = join[q][row_l];
+            for (int q = 0; q < 64; ++q) z[q] = q < cols ? z[q] : -INFINITY;
+          }
+          if constexpr (MODE == kStats) {
+            if (ycol >= 0) {
+              float zt = 0.0f;
+#pragma unroll
+              for (int q = 0; q < 64; ++q) zt = ycol == q ? z[q] : zt;
+              a.ztarget[row] = zt;
+            }
+            float mq[4] = {z[0], z[1], z[2], z[3]};  // four chains each: short waits
+#pragma unroll
+            for (int q = 4; q < 64; ++q) mq[q & 3] = fmaxf(mq[q & 3], z[q]);
+            const float m = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+            const float base = m > -INFINITY ? m * kLog2e : 0.0f;
+            float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int q = 0; q < 64; ++q) sq[q & 3] += ex2(fmaf(z[q], kLog2e, -base));
+            // the four warps of these rows; the first one writes the tile's pair
+            if (quarter != 0 && nth > 0 &&
+                !__all_sync(0xffffffffu, flow.wait(&join_free[quad], (nth - 1) & 1)))
+              break;
+            join[quarter][row_l] = make_float2(m, (sq[0] + sq[1]) + (sq[2] + sq[3]));
             __syncwarp();
-            if (lane == 0) mbar_arrive(&join_free[quad]);
-            const float nm = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-            const float nb = nm > -INFINITY ? nm * kLog2e : 0.0f;
-            float s = 0.0f;
+            if (lane == 0) mbar_arrive(&joined[quad]);
+            if (quarter == 0) {
+              if (!__all_sync(0xffffffffu, flow.wait(&joined[quad], nth & 1))) break;
+              float2 v[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) s = fmaf(v[q].y, ex2(fmaf(v[q].x, kLog2e, -nb)), s);
-            if (live) a.part[(size_t)j * a.N + row] = make_float2(nm, s);
-          }
-        } else {
+              for (int q = 0; q < 4; ++q) v[q] = join[q][row_l];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&join_free[quad]);
+              const float nm = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+              const float nb = nm > -INFINITY ? nm * kLog2e : 0.0f;
+              float s = 0.0f;
 #pragma unroll
-          for (int q = 0; q < 64; ++q) z[q] = ex2(fmaf(z[q], kLog2e, -lse2)) * g;
-          if (__any_sync(0xffffffffu, ycol >= 0)) {
+              for (int q = 0; q < 4; ++q) s = fmaf(v[q].y, ex2(fmaf(v[q].x, kLog2e, -nb)), s);
+              if (live) a.part[(size_t)j * a.N + row] = make_float2(nm, s);
+            }
+          } else {
 #pragma unroll
-            for (int q = 0; q < 64; ++q) z[q] -= q == ycol ? g : 0.0f;
-          }
-          for (int plane = 0; plane < a.planes; ++plane) {
-            staging_free(lane);
+            for (int q = 0; q < 64; ++q) z[q] = ex2(fmaf(z[q], kLog2e, -lse2)) * g;
+            if (__any_sync(0xffffffffu, ycol >= 0)) {
 #pragma unroll
-            for (int q = 0; q < 64; q += 8) {
-              uint32_t h[4];
+              for (int q = 0; q < 64; ++q) z[q] -= q == ycol ? g : 0.0f;
+            }
+            for (int plane = 0; plane < a.planes; ++plane) {
+              staging_free(lane);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t v = pack_bf16x2(z[q + 2 * e], z[q + 2 * e + 1]);
-                h[e] = zero ? 0u : v;  // whatever the row holds
-              }
-              sts128(staging_unit(box, lane, q / 8), make_uint4(h[0], h[1], h[2], h[3]));
-              if (plane + 1 < a.planes) {  // what the next plane holds
+              for (int q = 0; q < 64; q += 8) {
+                uint32_t h[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  z[q + 2 * e] -= __uint_as_float(h[e] << 16);
-                  z[q + 2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+                  const uint32_t v = pack_bf16x2(z[q + 2 * e], z[q + 2 * e + 1]);
+                  h[e] = zero ? 0u : v;  // whatever the row holds
+                }
+                sts128(staging_unit(box, lane, q / 8), make_uint4(h[0], h[1], h[2], h[3]));
+                if (plane + 1 < a.planes) {  // what the next plane holds
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    z[q + 2 * e] -= __uint_as_float(h[e] << 16);
+                    z[q + 2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+                  }
                 }
               }
-            }
-            staging_ready();
-            if (lane == 0 && row0 < a.N) {
-              tma_store_3d(&a.out[0], w.n * kBN + quarter * 64, row0, plane, box);
-              bulk_commit();
+              staging_ready();
+              if (lane == 0 && row0 < a.N) {
+                tma_store_3d(&a.out[0], w.n * kBN + quarter * 64, row0, plane, box);
+                bulk_commit();
+              }
             }
           }
-        }
       }
     }
     if (MODE != kStats && lane == 0) bulk_wait_all();

@@ -131,17 +131,19 @@ def test_many_tokens_per_block(rc):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-def test_ties_go_to_the_lowest_index(rc, dt):
-    z = torch.zeros(6, 24, device="cuda")
+@pytest.mark.parametrize("e", [24, 100, 256, 500])
+def test_ties_go_to_the_lowest_index(rc, dt, e):
+    z = torch.zeros(7, e, device="cuda")   # a router that starts at zero
     z[1, 5:9] = 1.0
-    z[2, ::2] = -0.0                    # equal to +0
+    z[2, ::2] = -0.0                       # equal to +0
     z[3] = -3.0
-    z[4, 23] = z[4, 0] = 7.0
-    z[5] = torch.arange(24, device="cuda") % 3
+    z[4, e - 1] = z[4, 0] = 7.0
+    z[5] = torch.arange(e, device="cuda") % 3
+    z[6, 8:16] = 2.0                       # more than a few neighbours
     z = [z.to(DT[dt])]
     g = Gate(rc, z, 5, norm=False)
     torch.cuda.synchronize()
-    check_forward(g, reference(z, 5, None, False, 0.02), z, 24)
+    check_forward(g, reference(z, 5, None, False, 0.02), z, e)
 
 
 @pytest.mark.parametrize("e,k", [(8, 3), (64, 8), (200, 8), (256, 16), (512, 16)])
@@ -184,13 +186,14 @@ def test_masked_tokens(rc, kind):
         assert bool(torch.isfinite(d[r]).all()) and bool((d[r][mask[r] == 0] == 0).all())
 
 
-def test_minus_infinity_and_non_finite_logits(rc):
-    e, k = 12, 4
-    z = make(1, 8, e, "f32", seed=9)[0]
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("e,k", [(12, 4), (100, 6), (256, 16), (400, 4)])
+def test_minus_infinity_and_non_finite_logits(rc, dt, e, k):
+    z = make(1, 8, e, dt, seed=9)[0]
     z[1] = -math.inf                     # an empty row
     z[2, 2:] = -math.inf                 # fewer experts than slots
     z[3, ::2] = -math.inf
-    z[4] = torch.finfo(torch.float32).min  # the type's lowest value is a number
+    z[4] = torch.finfo(DT[dt]).min       # the type's lowest value is a number
     g = Gate(rc, [z], k)
     torch.cuda.synchronize()
     check_forward(g, reference([z], k, None, True, 0.02), [z[[0, 1, 2, 3, 5, 6, 7]]], e)

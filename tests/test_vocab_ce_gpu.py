@@ -147,7 +147,17 @@ def test_few_tokens(rc, tokens, d, vocab, p, shift):
 
 def test_vocabulary_in_several_pieces(rc):
     """G exceeds one piece of the workspace: dhidden adds over the pieces, the last one shorter."""
-    c = Case(3000, 128, 20011, 4, seed=1)
+    c = Case(6000, 128, 30011, 4, seed=1)
+    c.forward(rc)
+    c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+    c.untouched()
+
+
+def test_few_tokens_and_a_vocabulary_in_several_pieces(rc):
+    """G in two planes, dhidden's sums kept per plane and added to over the pieces."""
+    c = Case(100, 48, 600007, 2, seed=15)
     c.forward(rc)
     c.backward(rc)
     rc.rc_stream_status()
