@@ -477,21 +477,22 @@ def _typed(x, dtype, shape, what: str) -> Optional[int]:
 _dtype_of = operator.attrgetter("dtype")
 
 
-def _typed_ptrs(xs, dtype, shapes, what: str):
-    """A pointer array (as bytes) of _typed addresses; shapes: one for all, or
-    a list of one for each.  With one shape, tensors after the first pass on
-    their type, element count and contiguity, checked for all at once."""
+def _typed_ptrs(xs, dtype, shape, what: str, counts=None):
+    """A pointer array (as bytes) of _typed addresses of one shape, or of
+    [counts[r], *shape[1:]] for each.  Tensors after the first pass on their
+    type, element count and contiguity, checked for all at once."""
     if xs is None:
         return None
     p = len(xs)
-    if not isinstance(shapes, list):
-        shapes = [shapes] * p
-        if p > 1 and dtype:
-            t = _torch_mod().Tensor
-            rest = xs[1:]
-            if list(map(type, rest)).count(t) == p - 1 and list(map(_dtype_of, rest)).count(dtype[0]) == p - 1 and \
-                    list(map(t.numel, rest)).count(math.prod(shapes[0])) == p - 1 and all(map(t.is_contiguous, rest)):
-                return struct.pack(f"{p}Q", _typed(xs[0], dtype, shapes[0], what), *map(t.data_ptr, rest))
+    if p > 1 and dtype:
+        t, rest = _torch_mod().Tensor, xs[1:]
+        if list(map(type, rest)).count(t) == p - 1 and list(map(_dtype_of, rest)).count(dtype[0]) == p - 1 and \
+                all(map(t.is_contiguous, rest)):
+            n = list(map(t.numel, rest))
+            if n.count(math.prod(shape)) == p - 1 if counts is None else n == [c * shape[1] for c in counts[1:]]:
+                first = shape if counts is None else (counts[0], *shape[1:])
+                return struct.pack(f"{p}Q", _typed(xs[0], dtype, first, what), *map(t.data_ptr, rest))
+    shapes = [shape] * p if counts is None else [(c, *shape[1:]) for c in counts]
     return struct.pack(f"{p}Q", *[_typed(x, dtype, s, what) for x, s in zip(xs, shapes)])
 
 
@@ -646,13 +647,14 @@ def _ce_sizes(hidden, weight, tokens, d, vocab, dtype):
             raise ValueError("tokens and d are required when buffers are raw addresses")
         tokens, d = hidden.shape
     if vocab is None:
-        if not all(_is_tensor(w) for w in weight):
+        if any(type(w) is int for w in weight):
             raise ValueError("vocab is required when weights are raw addresses")
-        vocab = sum(w.shape[0] for w in weight)
+        vocab = sum(map(_torch_mod().Tensor.numel, weight)) // int(d)
     p, dt = len(weight), _dt(dtype, hidden)
-    c = -(-int(vocab) // p)
-    shapes = [(max(0, min(int(vocab), (r + 1) * c) - r * c), int(d)) for r in range(p)]
-    return int(tokens), int(d), int(vocab), p, dt, shapes
+    vocab = int(vocab)
+    c = max(1, -(-vocab // p))           # rows of a full piece; then what is left, then none
+    rows = [c] * (vocab // c) + [vocab % c]
+    return int(tokens), int(d), vocab, p, dt, (rows + [0] * p)[:p]
 
 
 def _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, backward, stream):
@@ -668,11 +670,11 @@ def rc_vocab_ce_forward(hidden: Buf, weight: Sequence[Buf], target: Buf, loss: B
     """Cross entropy of every token over the ranks' vocabulary pieces:
     hidden [tokens, d], weight[r] [rows, d] (bf16), target (int32) [tokens];
     loss and lse (float32) [tokens] are written."""
-    t, d, v, p, dt, shapes = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
+    t, d, v, p, dt, rows = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
     f32, i32, _, kinds = _types()
     kind = kinds.get(dt, ())
     ws, nbytes, _keep = _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, False, stream)
-    _check(lib.rc_vocab_ce_forward(_typed(hidden, kind, (t, d), "hidden"), _typed_ptrs(weight, kind, shapes, "weight"),
+    _check(lib.rc_vocab_ce_forward(_typed(hidden, kind, (t, d), "hidden"), _typed_ptrs(weight, kind, (0, d), "weight", rows),
                                    _typed(target, i32, (t,), "target"), _typed(loss, f32, (t,), "loss"),
                                    _typed(lse, f32, (t,), "lse"), t, d, v, p, dt, int(ignore_index), ws, nbytes,
                                    _stream(stream)), "rc_vocab_ce_forward")
@@ -682,15 +684,15 @@ def rc_vocab_ce_backward(hidden: Buf, weight: Sequence[Buf], target: Buf, lse: B
                          dweight: Sequence[Buf], ignore_index: int = -100, workspace=None, tokens=None, d=None,
                          vocab=None, dtype=None, stream=None):
     """dhidden and dweight[r] from dloss (float32, [tokens]) and the forward's lse."""
-    t, d, v, p, dt, shapes = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
+    t, d, v, p, dt, rows = _ce_sizes(hidden, weight, tokens, d, vocab, dtype)
     _same_len(p, dweight=dweight)
     f32, i32, _, kinds = _types()
     kind = kinds.get(dt, ())
     ws, nbytes, _keep = _ce_workspace(workspace, hidden, weight, t, d, v, p, dt, True, stream)
-    _check(lib.rc_vocab_ce_backward(_typed(hidden, kind, (t, d), "hidden"), _typed_ptrs(weight, kind, shapes, "weight"),
+    _check(lib.rc_vocab_ce_backward(_typed(hidden, kind, (t, d), "hidden"), _typed_ptrs(weight, kind, (0, d), "weight", rows),
                                     _typed(target, i32, (t,), "target"), _typed(lse, f32, (t,), "lse"),
                                     _typed(dloss, f32, (t,), "dloss"), _typed(dhidden, kind, (t, d), "dhidden"),
-                                    _typed_ptrs(dweight, kind, shapes, "dweight"), t, d, v, p, dt, int(ignore_index),
+                                    _typed_ptrs(dweight, kind, (0, d), "dweight", rows), t, d, v, p, dt, int(ignore_index),
                                     ws, nbytes, _stream(stream)), "rc_vocab_ce_backward")
 
 

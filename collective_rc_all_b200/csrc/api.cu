@@ -1096,15 +1096,6 @@ rc_status rc_vocab_ce_backward(const void *hidden, const void *const *weight, co
   b.add(lse, tokens, 4, false, "lse", 0);
   b.add(dloss, tokens, 4, false, "dloss", 0);
   if ((st = check_all(b.bs)) != RC_OK) return st;
-  if (tokens == 0) {  // no token: the weights' gradient is zero
-    for (int r = 0; r < p; ++r) {
-      const uint64_t bytes = ce_rows(vocab, p, r) * d * 2;
-      if (!bytes) continue;
-      cudaError_t e = cudaMemsetAsync(dweight[r], 0, bytes, (cudaStream_t)stream);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
-    }
-    return RC_OK;
-  }
   return launched(launch_ce_backward(j, (cudaStream_t)stream), "vocab_ce_backward launch");
 }
 

@@ -949,6 +949,12 @@ __global__ void __launch_bounds__(kThreads) rc_ce_finish_kernel(const float *sum
   }
 }
 
+// No tokens: the weights' gradient is zero (rows of 2-byte elements).
+__global__ void __launch_bounds__(kThreads) rc_ce_zero_kernel(uint16_t *p, uint64_t n) {
+  pdl_wait();
+  for (uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (uint64_t)gridDim.x * kThreads) p[i] = 0;
+}
+
 // ---------------------------------------------------------------- host side
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -1223,6 +1229,17 @@ cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s) {
 }
 
 cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
+  if (j.shape.tokens == 0) {
+    const int64_t C = cdiv(j.shape.vocab, j.shape.p);
+    for (int64_t r = 0; r * C < j.shape.vocab; ++r) {
+      const uint64_t n = (uint64_t)std::min<int64_t>(C, j.shape.vocab - r * C) * j.shape.d;
+      const uint64_t grid = std::min<uint64_t>((n + kThreads - 1) / kThreads, (uint64_t)device_sm_count() * 8);
+      cudaError_t err = launch_kernel(rc_ce_zero_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s,
+                                      static_cast<uint16_t *>(j.dweight[r]), n);
+      if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+  }
   const bool copies = copies_needed(j);
   const Plan q = make_plan(j.shape, true, copies);
   char *ws = static_cast<char *>(j.ws);
