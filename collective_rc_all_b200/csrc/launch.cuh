@@ -10,8 +10,10 @@
 // memory only after everything earlier in the stream is finished, exactly as
 // with an ordinary launch; only the launch itself and the kernel's prologue
 // (index arithmetic, shared-memory set-up) overlap the previous kernel's
-// drain.  No kernel triggers its dependents early: they are released as its
-// blocks exit.  Stream capture turns the attribute into programmatic graph
+// drain.  Kernels release their dependents as their blocks exit, except those
+// of the cross entropy, whose blocks are all resident at once and which are a
+// chain of short launches: those release them before their last work
+// (pdl_release()).  Stream capture turns the attribute into programmatic graph
 // edges.
 //
 // Measured on the sequence of seven collectives captured in one graph
