@@ -61,8 +61,8 @@ struct GateParams {
   bool norm, vec;  // vec: rows are read and written as 16-byte vectors
 };
 
-// The row's values of this lane: experts [lane * VPL, lane * VPL + VPL);
-// those past E read as -inf.
+// The row's values of this lane: experts [lane * VPL, lane * VPL + VPL); those
+// past E are left as they are (-inf, see load_token).
 template <class T, int VPL>
 __device__ __forceinline__ void load_row(const char *row, int e0, int E, bool vec, float (&z)[VPL]) {
   constexpr int V = kVec<T>;
@@ -74,19 +74,18 @@ __device__ __forceinline__ void load_row(const char *row, int e0, int E, bool ve
         unpack<T>(ld_stream_v4(row + (uint64_t)(e0 + j) * T::kBytes), t);
 #pragma unroll
         for (int i = 0; i < V; ++i) z[j + i] = t[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) z[j + i] = -INFINITY;
       }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) z[j] = e0 + j < E ? load_elem<T>(row, e0 + j) : -INFINITY;
+    for (int j = 0; j < VPL; ++j)
+      if (e0 + j < E) z[j] = load_elem<T>(row, e0 + j);
   }
 }
 
 // The same for token t of a rank, whose row is at `row`; nothing but -inf when
-// there is no such token or it is masked.
+// there is no such token or it is masked.  The caller sets z to -inf once, before
+// its first token: the values past E stay so, and no token sets them again.
 template <class T, int VPL>
 __device__ __forceinline__ void load_token(const GateParams &a, const char *row, const uint8_t *mask, uint64_t t,
                                            int e0, float (&z)[VPL]) {
@@ -120,7 +119,8 @@ __device__ __forceinline__ float row_max(float v) {
 }
 
 // exp(z - m) as 2^((z - m) log2 e); the difference is exact where it matters
-// (z near m).  ex2.approx is within 2 units in the last place.
+// (z near m), and z log2 e by itself could pass the type's largest value.
+// ex2.approx is within 2 units in the last place.
 __device__ __forceinline__ float exp_diff(float z, float m) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((z - m) * kLog2e));
@@ -135,20 +135,26 @@ __device__ __forceinline__ float reciprocal(float x) {  // within one unit in th
 // What a row is without the experts that can't be chosen: NaN becomes -inf.
 __device__ __forceinline__ float choosable(float z) { return fmaxf(z, -INFINITY); }
 
-// ex = exp(z - top) of this lane's values, and the row's sum of them; `top` is
-// the row's largest number (-inf: it has none).  A row of -inf alone is not
-// live, and zero; a NaN, or +inf, makes the sum NaN.
+// The row's largest number (-inf: it has none).
 template <int LPT, int VPL>
-__device__ __forceinline__ float row_exp(const float (&z)[VPL], float top, float (&ex)[VPL], bool *live) {
-  const float base = top > -INFINITY ? top : 0.0f;
+__device__ __forceinline__ float row_top(const float (&z)[VPL]) {
+  float top = choosable(z[0]);
+#pragma unroll
+  for (int j = 1; j < VPL; ++j) top = fmaxf(top, z[j]);
+  return row_max<LPT>(top);
+}
+
+// ex = exp(z - base) of this lane's values and the lane's sum of them; base: the
+// row's largest number, or 0 where it has none.  The row's sum is NaN where it
+// holds a NaN or +inf; a row of -inf alone is zero.
+template <int VPL>
+__device__ __forceinline__ float lane_exp(const float (&z)[VPL], float base, float (&ex)[VPL]) {
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     ex[j] = exp_diff(z[j], base);
     s += ex[j];
   }
-  s = row_sum<LPT>(s);
-  *live = top > -INFINITY || isnan(s);
   return s;
 }
 
@@ -211,42 +217,72 @@ __device__ __forceinline__ void pick_exact(const float (&z)[VPL], int k, int e0,
 
 // With keys, for the long rows (16 and 32 lanes), where selects are what bounds
 // the kernel: a logit's bits as an ordered integer, the lowest 8 (9) replaced
-// by the index, lower indices larger.  Keys are all different, so the insertion
-// into a lane's three best is five minima and maxima, and a round is one
-// maximum over the lanes and three moves in the lane that has it.  slots.id
-// receives the k + 1 best keys.  Returns true where they may be wrong, and
-// pick_exact decides:
+// by the index, lower indices larger.  Keys are all different, so a lane's four
+// best come from a sorting network of minima and maxima (32 of them for 8
+// values), and a round is one maximum over the lanes and four moves in the lane
+// that has it.  slots.id receives the k + 1 best keys.  Returns true where they
+// may be wrong, and pick_exact decides:
 //  - two fp32 logits that differ in the dropped bits alone (a relative 2^-15)
 //    come out in index order: two neighbours among the k + 1 best agree in all
 //    other bits (bf16 logits keep all their bits);
 //  - -0 comes below +0: a zero is among them;
-//  - a lane holds its three best: one that has spent them may have had more.
+//  - a lane that has spent its four best may have had more.  (With three, one
+//    row in twelve of the 256 experts below had one; with four, one in 250.)
 // (The caller sees to rows with a NaN, whose keys are the largest.)
-// 131072 tokens x 256 experts, top 8, fp32: 120 us by pick_exact alone, 87 us
-// with keys (733 and 460 instructions per token; integer instructions bound
-// both, at 72% and 70% of the issue slots).
+// 131072 tokens x 256 experts, top 8, fp32: 120 us by pick_exact alone, 87 us with
+// keys and a lane's three best, 73 us with four and the rows read ahead straight
+// into the registers they are used from (bf16, 128 experts: 77 and 56 us for the
+// last two).  Integer instructions bound all of them, at 70% of the issue slots.
 constexpr uint32_t kFirstKey = 0x00800000u;  // of the lowest number; -inf lies below
 
-template <class T, int LPT, int VPL>
-__device__ __forceinline__ bool pick(const float (&z)[VPL], int k, int sub, int grp, Slots<LPT> &slots) {
+__device__ __forceinline__ void order(uint32_t &a, uint32_t &b) {  // the larger first
+  const uint32_t m = min(a, b);
+  a = max(a, b);
+  b = m;
+}
+// Leaves the four largest of v[0, N) in v[0, 4), sorted.
+template <int N>
+__device__ __forceinline__ void four_best(uint32_t *v) {
+  if constexpr (N == 4) {
+    order(v[0], v[1]);
+    order(v[2], v[3]);
+    order(v[0], v[2]);
+    order(v[1], v[3]);
+    order(v[1], v[2]);
+  } else {
+    four_best<N / 2>(v);
+    four_best<N / 2>(v + N / 2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = max(v[j], v[N / 2 + 3 - j]);  // the four, rising and falling
+    order(v[0], v[2]);
+    order(v[1], v[3]);
+    order(v[0], v[1]);
+    order(v[2], v[3]);
+  }
+}
+
+template <int LPT, int VPL>
+__device__ __forceinline__ void lane_best(const float (&z)[VPL], int sub, uint32_t (&best)[4]) {
   constexpr uint32_t kIndex = LPT * VPL <= 256 ? 255u : 511u;
-  constexpr uint32_t kSame = std::is_same<T, F32>::value ? kIndex : 0;  // bf16: what is alike is equal
-  uint32_t k1 = 0, k2 = 0, k3 = 0;
+  uint32_t v[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const uint32_t u = __float_as_uint(z[j]);
     const uint32_t ord = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-    const uint32_t v = (ord & ~kIndex) | (uint32_t)(VPL - 1 - j);
-    const uint32_t m1 = min(k1, v), m2 = min(k2, m1);
-    k1 = max(k1, v);
-    k2 = max(k2, m1);
-    k3 = max(k3, m2);
+    v[j] = (ord & ~kIndex) | (uint32_t)(VPL - 1 - j);
   }
+  four_best<VPL>(v);
   // the lane's part of the index (kIndex - e0 - j, and e0 = sub * VPL)
   const uint32_t part = kIndex - (uint32_t)(VPL - 1) - (uint32_t)sub * VPL;
-  k1 += part;
-  k2 += part;
-  k3 += part;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) best[j] = v[j] + part;
+}
+
+template <class T, int LPT, int VPL>
+__device__ __forceinline__ bool pick(const uint32_t (&mine)[4], int k, int sub, int grp, Slots<LPT> &slots) {
+  constexpr uint32_t kIndex = LPT * VPL <= 256 ? 255u : 511u;
+  constexpr uint32_t kSame = std::is_same<T, F32>::value ? kIndex : 0;  // bf16: what is alike is equal
+  uint32_t k1 = mine[0], k2 = mine[1], k3 = mine[2], k4 = mine[3];
   int32_t *out = slots.id[grp];
 #pragma unroll 4
   for (int i = 0; i <= k; ++i) {
@@ -262,7 +298,8 @@ __device__ __forceinline__ bool pick(const float (&z)[VPL], int k, int sub, int 
       out[i] = (int32_t)best;
       k1 = k2;
       k2 = k3;
-      k3 = 0;
+      k3 = k4;
+      k4 = 0;
     }
   }
   __syncwarp();
@@ -286,38 +323,49 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
   const uint64_t step = (uint64_t)blocks * kWarps * TPW;
   const char *rows = a.z[r];
   const uint8_t *mask = a.mask[r];
-  int32_t *ids = a.ids[r];
-  float *weights = a.w[r];
   const int k = a.k;
   float *row_buf = buf + warp * 32 * VPL;
   uint64_t t = ((uint64_t)block * kWarps + warp) * TPW + grp;
+  int32_t *ids = a.ids[r] + t * k + sub;
+  float *weights = a.w[r] + t * k + sub;
+  const uint64_t out_step = step * k;
   float next[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) next[j] = -INFINITY;
   const char *row = rows + t * (uint64_t)a.E * T::kBytes;
   const uint64_t row_step = step * (uint64_t)a.E * T::kBytes;
   load_token<T, VPL>(a, row, mask, t, e0, next);
-  for (; t - grp < a.tokens; t += step) {
+  for (; t - grp < a.tokens; t += step, ids += out_step, weights += out_step) {
     const bool have = t < a.tokens;
     row += row_step;
-    float z[VPL], ex[VPL];
+    float z[VPL], ex[VPL];  // z: short rows only (long ones lie in row_buf)
+    const float top = row_top<LPT>(next), base = top > -INFINITY ? top : 0.0f;
+    float total = lane_exp(next, base, ex);
+    uint32_t best[4];
+    if constexpr (LPT >= kMaxK) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) z[j] = next[j];
+      for (int j = 0; j < VPL; j += 4)
+        *reinterpret_cast<float4 *>(&row_buf[lane * VPL + j]) =
+            make_float4(next[j], next[j + 1], next[j + 2], next[j + 3]);
+      lane_best<LPT, VPL>(next, sub, best);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) z[j] = next[j];
+    }
     load_token<T, VPL>(a, row, mask, t + step, e0, next);  // in flight while this one is worked on
-    float top = choosable(z[0]);
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) top = fmaxf(top, z[j]);
-    top = row_max<LPT>(top);
-    bool live;
-    const float total = row_exp<LPT, VPL>(z, top, ex, &live);
+    total = row_sum<LPT>(total);
+    const bool live = top > -INFINITY || isnan(total);
     const float inv = live ? reciprocal(total) : 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) sum.p[j] = fmaf(ex[j], inv, sum.p[j]);
     sum.tokens += (live && sub == 0) ? 1 : 0;
     bool exact = true;
     if constexpr (LPT >= kMaxK) {
+      exact = __any_sync(0xffffffffu, pick<T, LPT, VPL>(best, k, sub, grp, slots) || isnan(total));
+      if (exact) {
 #pragma unroll
-      for (int j = 0; j < VPL; j += 4)
-        *reinterpret_cast<float4 *>(&row_buf[lane * VPL + j]) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
-      exact = __any_sync(0xffffffffu, pick<T, LPT, VPL>(z, k, sub, grp, slots) || isnan(total));
+        for (int j = 0; j < VPL; ++j) z[j] = row_buf[lane * VPL + j];
+      }
     }
     if (exact) pick_exact<LPT, VPL>(z, k, e0, grp, slots);
     __syncwarp();
@@ -336,7 +384,7 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
         id[q] = (uint32_t)id[q] >= kFirstKey ? kIndex - (id[q] & kIndex) : -1;
         v = id[q] >= 0 ? row_buf[grp * LPT * VPL + id[q]] : 0.0f;
       }
-      w[q] = id[q] >= 0 ? exp_diff(v, top) : 0.0f;
+      w[q] = id[q] >= 0 ? exp_diff(v, base) : 0.0f;
       share += w[q];
       if (id[q] >= 0) atomicAdd(&count[id[q]], 1);  // integers: any order gives the same sum
     }
@@ -350,8 +398,8 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
       for (int q = 0; q < kMine; ++q) {
         const int i = sub + q * LPT;
         if (i < k) {
-          ids[t * k + i] = id[q];
-          weights[t * k + i] = id[q] < 0 ? 0.0f : w[q] * per;
+          ids[q * LPT] = id[q];
+          weights[q * LPT] = id[q] < 0 ? 0.0f : w[q] * per;
         }
       }
     }
@@ -561,8 +609,15 @@ __global__ void __cluster_dims__(kStatBlocks, 1, 1) __launch_bounds__(kStatNT)
 // dz of one token: with a_e = dloss * coef * E * f_e / M, S = the chosen
 // experts' probabilities, and q_i = p_i / S (normalised) or p_i:
 //   dz = p (a - sum p a) + [chosen] q dw - (normalised: [chosen] q, else p) * sum_i q_i dw_i
+// Blocks per SM that the registers are cut to: 8 x 16384 x 256 fp32 67 us with the
+// compiler's own 72 registers and three blocks, 59 us with four; with 8 lanes the
+// two slots ahead take more registers than a fourth block is worth (71, 73 us for
+// both passes of 8 x 16384 x 64), with 16 values one block more spills (158, 205
+// us for both passes of 8 x 8192 x 512).
+constexpr int back_blocks(int lpt, int vpl) { return vpl > 8 ? 2 : lpt == 8 ? 3 : 4; }
+
 template <class T, int LPT, int VPL>
-__global__ void __launch_bounds__(kBackNT) rc_gate_backward_kernel(const __grid_constant__ GateParams a) {
+__global__ void __launch_bounds__(kBackNT, back_blocks(LPT, VPL)) rc_gate_backward_kernel(const __grid_constant__ GateParams a) {
   constexpr int TPW = 32 / LPT;
   constexpr int V = kVec<T>;
   constexpr uint32_t kNone = 0x7fffffffu;  // marks experts that were not chosen
@@ -582,36 +637,62 @@ __global__ void __launch_bounds__(kBackNT) rc_gate_backward_kernel(const __grid_
   const uint64_t step = (uint64_t)gridDim.x * kBackWarps * TPW;
   const char *rows = a.z[r];
   const uint8_t *mask = a.mask[r];
-  const int32_t *ids = a.ids[r];
-  const float *dw = a.dw[r];
   char *dz = a.dz[r];
   const int k = a.k;
   uint64_t t = ((uint64_t)blockIdx.x * kBackWarps + warp) * TPW + grp;
+  // the chosen experts and their gradients, one token ahead like its row: slots
+  // sub, sub + LPT, ...
+  constexpr int kMine = LPT >= kMaxK ? 1 : kMaxK / LPT;
+  constexpr int kAhead = kMine <= 2 ? kMine : 0;  // (more would take the registers; read ahead 138 us for both passes
+                                                  // of 8 x 16384 x 256 fp32, in their own turn 145)
+  const int32_t *ids = a.ids[r] + t * k + sub;
+  const float *dw = a.dw[r] == nullptr ? nullptr : a.dw[r] + t * k + sub;
+  const uint64_t out_step = step * k;
+  int32_t next_id[kAhead + 1];
+  float next_dw[kAhead + 1];
+  auto load_chosen = [&](bool there) {  // (a masked token's ids are -1)
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const bool in = there && dw != nullptr && sub + q * LPT < k;
+      next_id[q] = in ? ids[q * LPT] : -1;
+      next_dw[q] = in ? dw[q * LPT] : 0.0f;
+    }
+  };
   float next[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) next[j] = -INFINITY;
   const char *row = rows + t * (uint64_t)a.E * T::kBytes;
   const uint64_t row_step = step * (uint64_t)a.E * T::kBytes;
   load_token<T, VPL>(a, row, mask, t, e0, next);
+  load_chosen(t < a.tokens);
   for (; t - grp < a.tokens; t += step) {
     const bool have = t < a.tokens;
     char *out = dz + (row - rows);
     row += row_step;
     float z[VPL], p[VPL];
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) z[j] = next[j];
+    const float top = row_top<LPT>(next), base = top > -INFINITY ? top : 0.0f;
+    float total = lane_exp(next, base, p);
     __syncwarp();
-    if (have && dw != nullptr) {  // (a masked token's ids are -1)
-      for (int i = sub; i < k; i += LPT) {
-        const int id = ids[t * k + i];
-        if (id >= 0 && id < a.E) row_grad[id] = __float_as_uint(dw[t * k + i]);
+    if constexpr (kAhead > 0) {
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+        if (next_id[q] >= 0 && next_id[q] < a.E) row_grad[next_id[q]] = __float_as_uint(next_dw[q]);
+      ids += out_step;
+      if (dw != nullptr) dw += out_step;
+      load_chosen(t + step < a.tokens);
+    } else {
+      if (have && dw != nullptr) {
+        for (int i = 0; sub + i < k; i += LPT) {
+          const int id = ids[i];
+          if (id >= 0 && id < a.E) row_grad[id] = __float_as_uint(dw[i]);
+        }
+        dw += out_step;
       }
+      ids += out_step;
     }
     load_token<T, VPL>(a, row, mask, t + step, e0, next);  // in flight while this one is worked on
-    float top = choosable(z[0]);
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) top = fmaxf(top, z[j]);
-    top = row_max<LPT>(top);
-    bool live;
-    const float total = row_exp<LPT, VPL>(z, top, p, &live);
+    total = row_sum<LPT>(total);
+    const bool live = top > -INFINITY || isnan(total);
     const float inv = live ? reciprocal(total) : 0.0f;
     __syncwarp();
     uint32_t g[VPL];
