@@ -164,6 +164,50 @@ def test_neighbours_that_differ_in_the_last_bits(rc, e, k, sign):
     check_forward(g, reference([z], k, None, True, 0.02), [z], e)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("e,k", [(64, 8), (100, 8), (128, 16), (200, 8), (256, 16), (512, 16)])
+def test_best_experts_are_neighbours(rc, dt, e, k):
+    """The k best in a run of k neighbours (at any offset), in any order, and by halves in two runs."""
+    t = 48
+    gen = torch.Generator(device="cuda").manual_seed(e + k)
+    z = torch.randn(t, e, generator=gen, device="cuda")
+    for i in range(t):
+        at = i * (e - k) // (t - 1)
+        up = 8.0 + torch.randperm(k, generator=gen, device="cuda").float() / 4
+        if i % 3 == 2:
+            z[i, at:at + k // 2] = up[:k // 2]
+            z[i, (at + e // 2) % (e - k):][:k // 2] = up[k // 2:]
+        else:
+            z[i, at:at + k] = up
+    z = [z.to(DT[dt])]
+    g = Gate(rc, z, k)
+    torch.cuda.synchronize()
+    check_forward(g, reference(z, k, None, True, 0.02), z, e)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("e", [6, 20, 60, 128, 256, 400])
+def test_extreme_logits(rc, dt, e):
+    """Masks of the type's lowest value, and its largest: differences of 0 and beyond exp's range."""
+    lim = torch.finfo(DT[dt])
+    z = torch.full((5, e), lim.min, device="cuda", dtype=DT[dt])
+    z[1, 4] = 0.5                    # the rest is masked
+    z[2, 2] = lim.max                # the rest is far below
+    z[3] = lim.max
+    z[4, :3] = torch.tensor([1.0, 3.0, 2.0], device="cuda")
+    g = Gate(rc, [z], 2, norm=False)
+    d = torch.empty_like(z)
+    dw = torch.ones(5, 2, device="cuda")
+    rc.rc_moe_gate_backward([z], g.ids, g.stats, [d], dweights=[dw], normalize=False, coef=0.0)
+    torch.cuda.synchronize()
+    assert g.ids[0].tolist() == [[0, 1], [4, 0], [2, 0], [0, 1], [1, 2]]
+    low = [math.exp(-2), 1.0, math.exp(-1)]
+    want = torch.tensor([[1 / e] * 2, [1, 0], [1, 0], [1 / e] * 2, [1 / sum(low), low[2] / sum(low)]], dtype=torch.float64)
+    # every row has at most three different values: the sum (E U), expf, its argument (2 U) and the quotient
+    assert bool((g.weights[0].double().cpu() - want).abs().le((e + 16) * U * want).all())
+    assert bool(torch.isfinite(d).all()) and bool((d[1:3] == 0).all())
+
+
 @pytest.mark.parametrize("kind", ["some", "one_rank", "all"])
 def test_masked_tokens(rc, kind):
     p, t, e, k = 3, 50, 20, 3
@@ -270,6 +314,39 @@ def test_backward(rc, dt, p, t, e, k, norm):
         got = d[r][0].double().cpu().numpy()
         assert np.all(np.abs(got - want[r]) <= rel * size[r] + half * (np.abs(want[r]) + rel * size[r]) + 1e-37)
     untouched(d)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("t,e,k", [(90000, 16, 2), (40000, 30, 4), (25000, 64, 8), (12000, 100, 6), (7000, 200, 8), (7000, 400, 16)])
+def test_backward_of_many_tokens(rc, dt, t, e, k):
+    """More tokens than the grid takes in one step, with masked ones between."""
+    p = 4
+    z = make(p, t, e, dt, seed=e)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    dw = [torch.randn(t, k, generator=gen, device="cuda") for _ in range(p)]
+    mask = [torch.rand(t, generator=gen, device="cuda") > 0.1 for _ in range(p)]
+    dloss = torch.full((1,), 2.0, device="cuda")
+    g = Gate(rc, z, k, mask=mask, coef=0.5)
+    d = [torch.empty_like(x) for x in z]
+    rc.rc_moe_gate_backward(z, g.ids, g.stats, d, dweights=dw, dloss=dloss, token_mask=mask, coef=0.5)
+    torch.cuda.synchronize()
+    f = sum(torch.bincount(x[x >= 0].long(), minlength=e) for x in g.ids).double() / (k * sum(int(m.sum()) for m in mask))
+    a = 2.0 * 0.5 * e * f / sum(int(m.sum()) for m in mask)
+    rel, half = 6 * (spread(z) + e + 24) * U, torch.finfo(DT[dt]).eps / 2  # as above
+    for r in range(p):
+        prob = torch.softmax(z[r].double(), 1)
+        at = torch.sort(-z[r].double(), dim=1, stable=True).indices[:, :k]
+        w = prob.gather(1, at)
+        w = w / w.sum(1, keepdim=True)
+        d64 = dw[r].double()
+        inner, outer = (w * d64).sum(1, keepdim=True), (w * d64.abs()).sum(1, keepdim=True)
+        want = prob * (a - (prob @ a)[:, None])
+        size = prob * (a + (prob @ a)[:, None])
+        want.scatter_add_(1, at, w * (d64 - inner))
+        size.scatter_add_(1, at, w * (d64.abs() + outer))
+        want[~mask[r]] = size[~mask[r]] = 0.0
+        assert bool((g.ids[r][mask[r]] == at[mask[r]]).all())
+        assert bool(((d[r].double() - want).abs() <= rel * size + half * (want.abs() + rel * size) + 1e-37).all())
 
 
 @pytest.mark.parametrize("norm", [False, True])
