@@ -110,6 +110,7 @@ struct alignas(64) CeParams {
   int tpr;                    // 256-row tiles per rank
   int j0;                     // first tile of this launch's piece
   int planes;                 // bf16 planes of G
+  int h_rows;                 // kStats, kGrad: rows in a copy of h
   int chunk;                  // kStats, kGrad: steps of k that one accumulator sums
   int heavy, quota;           // kBack: the schedule (see tile_of)
   int ignore;
@@ -316,11 +317,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
         // hundred cycles for each, and a division would take most of them
         const CUtensorMap *bmap = &a.b[0];
         int plane = 0, kk = w.k0, row = 0, left = 0, r = 0, per_plane = 0;
+        bool h_here = true;
+        uint32_t bytes = 2 * kStageBytes;
         if constexpr (LOGITS) {
           const int j = a.j0 + w.n;
           r = j / a.tpr;
           bmap = &a.b[r];
           row = (j - r * a.tpr) * kBN + (int)c * kHalf;
+          if (a.h_rows < kHalf) {
+            h_here = c == 0;
+            bytes = 2 * kOpBytes + (uint32_t)a.h_rows * (kBK * 2);
+          }
         } else {
           if (!w.dw && a.stacked) {
             per_plane = a.main.nk;
@@ -339,10 +346,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kNT, 1)
           }
           const uint32_t sa = smem0 + slot * kStageBytes, sb = sa + kOpBytes;
           // both blocks' bytes are counted on the first block's barrier
-          if (c == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStageBytes);
+          if (c == 0) mbar_arrive_expect_tx(&full[slot], bytes);
           const uint32_t bar = full0 + slot * 8;
           if constexpr (LOGITS) {
-            tma_load_2d(sa, &a.a, k * kBK, am, bar);
+            if (h_here) tma_load_2d(sa, &a.a, k * kBK, am, bar);
             tma_load_2d(sb, bmap, k * kBK, row, bar);
           } else {
             if (w.dw) {
@@ -1090,6 +1097,14 @@ Plan make_plan(const CeShape &s, bool backward, bool copies) {
   return q;
 }
 
+// Rows in a copy of h for the logits.  Up to 16 tokens only those that are there
+// (in whole periods of the swizzle), and none by the second block: whatever the
+// other rows hold stays in their own rows of the tile, which nobody takes.
+// Loss alone, 4096 x 32000 and 1024 x 128000, whole copies and these: 8 tokens
+// 78 and 75 us, 60 and 58; 16 tokens 57 and 69, 61 and 59; 64 tokens 57 and 55, 61
+// and 59.
+int h_rows(int64_t tokens) { return tokens <= 16 ? (int)up(tokens, 8) : kHalf; }
+
 // Devices on which each tile kernel has been allowed its shared memory.
 std::atomic<uint64_t> g_smem_ready[3];
 
@@ -1226,7 +1241,8 @@ cudaError_t launch_ce_forward(const CeJob &j, cudaStream_t s) {
     Operands o{};
     if ((err = operands(j, q, copies, &o, a.rows, s)) != cudaSuccess) return err;
     const int D = j.shape.d;
-    bool ok = make_map(&a.a, o.h, 0, N, D, o.pitch, kHalf);
+    a.h_rows = h_rows(N);
+    bool ok = make_map(&a.a, o.h, 0, N, D, o.pitch, a.h_rows);
     for (int r = 0; r < q.ranks; ++r) ok = ok && make_map(&a.b[r], o.w[r], 0, a.rows[r], D, o.pitch, kHalf);
     if (!ok) return cudaErrorInvalidValue;
     a.target = j.target;
@@ -1284,6 +1300,7 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
   z.ignore = j.ignore;
   z.V = (int)j.shape.vocab;
   z.chunk = q.planes == 2 ? kChunk : (int)cdiv(D, kBK);
+  z.h_rows = h_rows(N);
   CeParams w = z;  // dh and dW
   w.dw_tma = D % 8 == 0;
   for (int r = 0; r < q.ranks; ++r) {
@@ -1294,7 +1311,7 @@ cudaError_t launch_ce_backward(const CeJob &j, cudaStream_t s) {
   w.direct = q.pieces == 1 && q.slots == 1 && dh_aligned;
   w.stacked = q.stacked;
   const char *const h = ws + q.off_h;
-  bool ok = make_map(&z.a, o.h, 0, N, D, o.pitch, kHalf) && make_map(&w.wb, h, 0, N, D, q.dpad, 64) &&
+  bool ok = make_map(&z.a, o.h, 0, N, D, o.pitch, z.h_rows) && make_map(&w.wb, h, 0, N, D, q.dpad, 64) &&
             (w.direct ? make_map(&w.dh, j.dhidden, 0, N, D, D, 32)
                       : make_map(&w.dh, sums, q.slots, N, D, q.dpad, 32, true));
   for (int r = 0; r < q.ranks; ++r) {
