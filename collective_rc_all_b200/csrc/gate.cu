@@ -166,6 +166,16 @@ struct Sums {
   int32_t tokens;
 };
 
+// A lane's places among the chosen: sub, sub + LPT, ...
+constexpr int slots_per_lane(int lpt) { return lpt >= kMaxK ? 1 : lpt == 1 ? 8 : kMaxK / lpt; }
+
+// Which rows are chosen from by keys (see pick), the others by value alone: those
+// of 16 and 32 lanes, and of 4 and 8 from three choices on.  8 x 16384 tokens,
+// forward, by value and by keys: 64 experts, top 8, fp32 51 and 30 us; top 2,
+// bf16 22 and 23; 30 experts, top 8, fp32 36 and 22; 32 experts, top 2, bf16 15
+// and 16.5.
+constexpr bool by_keys(int lpt, int k) { return lpt >= 16 || (lpt >= 4 && k > 2); }
+
 template <int LPT>
 struct Slots {  // the chosen experts of the tokens that a warp is at
   static constexpr int kSlots = LPT == 1 ? 8 : kMaxK + 1;  // 8 experts at most have a lane per token
@@ -215,13 +225,13 @@ __device__ __forceinline__ void pick_exact(const float (&z)[VPL], int k, int e0,
   }
 }
 
-// With keys, for the long rows (16 and 32 lanes), where selects are what bounds
-// the kernel: a logit's bits as an ordered integer, the lowest 8 (9) replaced
-// by the index, lower indices larger.  Keys are all different, so a lane's four
-// best come from a sorting network of minima and maxima (32 of them for 8
-// values), and a round is one maximum over the lanes and four moves in the lane
-// that has it.  slots.id receives the k + 1 best keys.  Returns true where they
-// may be wrong, and pick_exact decides:
+// With keys, where selects are what bounds the kernel: a logit's bits as an
+// ordered integer, the lowest ones replaced by the index, lower indices larger.
+// Keys are all different, so a lane's best (four, or all eight where few lanes
+// share the choices) come from a sorting network of minima and maxima (32 of
+// them for four of 8 values), and a round is one maximum over the lanes and a
+// move per key in the lane that has it.  slots.id receives the k + 1 best keys.
+// Returns true where they may be wrong, and pick_exact decides:
 //  - two fp32 logits that differ in the dropped bits alone (a relative 2^-15)
 //    come out in index order: two neighbours among the k + 1 best agree in all
 //    other bits (bf16 logits keep all their bits);
@@ -260,10 +270,25 @@ __device__ __forceinline__ void four_best(uint32_t *v) {
     order(v[2], v[3]);
   }
 }
+// Sorts v[0, 8): two sorted halves, merged.
+__device__ __forceinline__ void sort_eight(uint32_t *v) {
+  four_best<4>(v);
+  four_best<4>(v + 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) order(v[j], v[j + 4]);
+  order(v[2], v[4]);
+  order(v[3], v[5]);
+  order(v[1], v[2]);
+  order(v[3], v[4]);
+  order(v[5], v[6]);
+}
+
+// How many of its values a lane keeps: all where few lanes share the choices.
+constexpr int kept(int lpt) { return lpt >= 16 ? 4 : 8; }
 
 template <int LPT, int VPL>
-__device__ __forceinline__ void lane_best(const float (&z)[VPL], int sub, uint32_t (&best)[4]) {
-  constexpr uint32_t kIndex = LPT * VPL <= 256 ? 255u : 511u;
+__device__ __forceinline__ void lane_best(const float (&z)[VPL], int sub, uint32_t (&best)[kept(LPT)]) {
+  constexpr uint32_t kIndex = LPT * VPL - 1;  // (a power of two less one)
   uint32_t v[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
@@ -271,41 +296,47 @@ __device__ __forceinline__ void lane_best(const float (&z)[VPL], int sub, uint32
     const uint32_t ord = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     v[j] = (ord & ~kIndex) | (uint32_t)(VPL - 1 - j);
   }
-  four_best<VPL>(v);
+  if constexpr (kept(LPT) == 8) {
+    static_assert(VPL == 8, "a lane keeps all of its values");
+    sort_eight(v);
+  } else {
+    four_best<VPL>(v);
+  }
   // the lane's part of the index (kIndex - e0 - j, and e0 = sub * VPL)
   const uint32_t part = kIndex - (uint32_t)(VPL - 1) - (uint32_t)sub * VPL;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) best[j] = v[j] + part;
+  for (int j = 0; j < kept(LPT); ++j) best[j] = v[j] + part;
 }
 
 template <class T, int LPT, int VPL>
-__device__ __forceinline__ bool pick(const uint32_t (&mine)[4], int k, int sub, int grp, Slots<LPT> &slots) {
-  constexpr uint32_t kIndex = LPT * VPL <= 256 ? 255u : 511u;
+__device__ __forceinline__ bool pick(uint32_t (&mine)[kept(LPT)], int k, int sub, int grp, Slots<LPT> &slots) {
+  constexpr uint32_t kIndex = LPT * VPL - 1;
   constexpr uint32_t kSame = std::is_same<T, F32>::value ? kIndex : 0;  // bf16: what is alike is equal
-  uint32_t k1 = mine[0], k2 = mine[1], k3 = mine[2], k4 = mine[3];
   int32_t *out = slots.id[grp];
 #pragma unroll 4
   for (int i = 0; i <= k; ++i) {
     uint32_t best;
     if constexpr (LPT == 32) {
-      best = __reduce_max_sync(0xffffffffu, k1);
+      best = __reduce_max_sync(0xffffffffu, mine[0]);
     } else {
-      best = k1;
+      best = mine[0];
 #pragma unroll
       for (int d = LPT / 2; d > 0; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
     }
-    if (k1 == best) {  // one lane; or all of them, with nothing left (0)
+    if (mine[0] == best) {  // one lane; or all of them, with nothing left (0)
       out[i] = (int32_t)best;
-      k1 = k2;
-      k2 = k3;
-      k3 = k4;
-      k4 = 0;
+#pragma unroll
+      for (int j = 1; j < kept(LPT); ++j) mine[j - 1] = mine[j];
+      mine[kept(LPT) - 1] = 0;
     }
   }
   __syncwarp();
-  bool doubt = k1 == 0;
-  if (sub < k) {
-    const uint32_t a = (uint32_t)out[sub], b = (uint32_t)out[sub + 1];
+  bool doubt = kept(LPT) < VPL && mine[0] == 0;
+#pragma unroll
+  for (int q = 0; q < slots_per_lane(LPT); ++q) {
+    const int i = sub + q * LPT;
+    if (i >= k) break;
+    const uint32_t a = (uint32_t)out[i], b = (uint32_t)out[i + 1];
     // (a pair below kFirstKey is two of -inf: equal, and not chosen)
     doubt = doubt || (a >= kFirstKey && ((a ^ b) <= kSame || b - (0x7fffffffu - kIndex) <= 2 * kIndex + 1 ||
                                          a - (0x7fffffffu - kIndex) <= 2 * kIndex + 1));
@@ -314,7 +345,7 @@ __device__ __forceinline__ bool pick(const uint32_t (&mine)[4], int k, int sub, 
 }
 
 // The tokens of rank r that fall to this block.
-template <class T, int LPT, int VPL>
+template <class T, int LPT, int VPL, bool KEYS>
 __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int blocks, Slots<LPT> &slots,
                                      float *buf, int32_t *count, Sums<VPL> &sum) {
   constexpr int TPW = 32 / LPT;  // tokens per warp and step
@@ -338,11 +369,11 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
   for (; t - grp < a.tokens; t += step, ids += out_step, weights += out_step) {
     const bool have = t < a.tokens;
     row += row_step;
-    float z[VPL], ex[VPL];  // z: short rows only (long ones lie in row_buf)
+    float z[VPL], ex[VPL];  // z: without keys (else the rows lie in row_buf)
     const float top = row_top<LPT>(next), base = top > -INFINITY ? top : 0.0f;
     float total = lane_exp(next, base, ex);
-    uint32_t best[4];
-    if constexpr (LPT >= kMaxK) {
+    [[maybe_unused]] uint32_t best[kept(LPT)];
+    if constexpr (KEYS) {
 #pragma unroll
       for (int j = 0; j < VPL; j += 4)
         *reinterpret_cast<float4 *>(&row_buf[lane * VPL + j]) =
@@ -360,7 +391,7 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
     for (int j = 0; j < VPL; ++j) sum.p[j] = fmaf(ex[j], inv, sum.p[j]);
     sum.tokens += (live && sub == 0) ? 1 : 0;
     bool exact = true;
-    if constexpr (LPT >= kMaxK) {
+    if constexpr (KEYS) {
       exact = __any_sync(0xffffffffu, pick<T, LPT, VPL>(best, k, sub, grp, slots) || isnan(total));
       if (exact) {
 #pragma unroll
@@ -369,7 +400,7 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
     }
     if (exact) pick_exact<LPT, VPL>(z, k, e0, grp, slots);
     __syncwarp();
-    constexpr int kMine = LPT >= kMaxK ? 1 : LPT == 1 ? 8 : kMaxK / LPT;  // slots of a lane: sub, sub + LPT, ...
+    constexpr int kMine = slots_per_lane(LPT);
     int id[kMine];
     float w[kMine], share = 0.0f;
 #pragma unroll
@@ -379,8 +410,8 @@ __device__ __forceinline__ void walk(const GateParams &a, int r, int block, int 
       float v = 0.0f;
       if (exact) {
         v = i < k ? slots.z[grp][i] : 0.0f;
-      } else if constexpr (LPT >= kMaxK) {
-        constexpr int kIndex = LPT * VPL <= 256 ? 255 : 511;
+      } else if constexpr (KEYS) {
+        constexpr int kIndex = LPT * VPL - 1;
         id[q] = (uint32_t)id[q] >= kFirstKey ? kIndex - (id[q] & kIndex) : -1;
         v = id[q] >= 0 ? row_buf[grp * LPT * VPL + id[q]] : 0.0f;
       }
@@ -452,22 +483,22 @@ __device__ __forceinline__ void clear(Sums<VPL> &sum, int32_t *count, int n) {
 
 __device__ __forceinline__ float warp_sum(float v) { return row_sum<32>(v); }
 
-// A block's buffer: the rows that its warps are at (long rows only, see pick),
+// A block's buffer: the rows that its warps are at (with keys, see pick),
 // then the warps' sums.
-template <int LPT, int VPL>
+template <int LPT, int VPL, bool KEYS>
 constexpr int buf_floats() {
-  return kWarps * (LPT >= kMaxK ? 32 : LPT) * VPL;
+  return kWarps * (KEYS ? 32 : LPT) * VPL;
 }
 
-template <class T, int LPT, int VPL>
-__global__ void __launch_bounds__(kNT) rc_gate_kernel(const __grid_constant__ GateParams a) {
-  __shared__ __align__(16) float buf[buf_floats<LPT, VPL>()];
+template <class T, int LPT, int VPL, bool KEYS>
+__global__ void __launch_bounds__(kNT, VPL > 8 ? 1 : 2) rc_gate_kernel(const __grid_constant__ GateParams a) {
+  __shared__ __align__(16) float buf[buf_floats<LPT, VPL, KEYS>()];
   __shared__ Slots<LPT> slots[kWarps];
   __shared__ int32_t tok[kWarps], count[LPT * VPL];
   Sums<VPL> sum;
   clear(sum, count, LPT * VPL);
   pdl_wait();
-  walk<T, LPT, VPL>(a, blockIdx.y, blockIdx.x, gridDim.x, slots[threadIdx.x >> 5], buf, count, sum);
+  walk<T, LPT, VPL, KEYS>(a, blockIdx.y, blockIdx.x, gridDim.x, slots[threadIdx.x >> 5], buf, count, sum);
   const uint64_t b = (uint64_t)blockIdx.y * gridDim.x + blockIdx.x;
   const int32_t tokens = gather_block<LPT>(sum, buf, tok, a.E, [&](int e, float p) {
     a.part[b * a.E + e] = make_float2(p, __int_as_float(count[e]));
@@ -478,7 +509,8 @@ __global__ void __launch_bounds__(kNT) rc_gate_kernel(const __grid_constant__ Ga
 // Few tokens: one block walks all ranks and finishes by itself.
 template <class T, int LPT, int VPL>
 __global__ void __launch_bounds__(kNT) rc_gate_one_kernel(const __grid_constant__ GateParams a) {
-  __shared__ __align__(16) float buf[buf_floats<LPT, VPL>()];
+  constexpr bool KEYS = by_keys(LPT, 1);
+  __shared__ __align__(16) float buf[buf_floats<LPT, VPL, KEYS>()];
   __shared__ Slots<LPT> slots[kWarps];
   __shared__ int32_t tok[kWarps], count[LPT * VPL];
   __shared__ float total_p[LPT * VPL], dots[kWarps];
@@ -488,7 +520,7 @@ __global__ void __launch_bounds__(kNT) rc_gate_one_kernel(const __grid_constant_
   for (int r = 0; r < a.p; ++r) {
     Sums<VPL> sum;
     clear(sum, count, LPT * VPL);
-    walk<T, LPT, VPL>(a, r, 0, 1, slots[threadIdx.x >> 5], buf, count, sum);
+    walk<T, LPT, VPL, KEYS>(a, r, 0, 1, slots[threadIdx.x >> 5], buf, count, sum);
     m += gather_block<LPT>(sum, buf, tok, a.E, [&](int e, float p) {  // thread e % kNT only
       const int32_t c = count[e];
       a.counts[r][e] = c;
@@ -642,7 +674,7 @@ __global__ void __launch_bounds__(kBackNT, back_blocks(LPT, VPL)) rc_gate_backwa
   uint64_t t = ((uint64_t)blockIdx.x * kBackWarps + warp) * TPW + grp;
   // the chosen experts and their gradients, one token ahead like its row: slots
   // sub, sub + LPT, ...
-  constexpr int kMine = LPT >= kMaxK ? 1 : kMaxK / LPT;
+  constexpr int kMine = slots_per_lane(LPT);
   constexpr int kAhead = kMine <= 2 ? kMine : 0;  // (more would take the registers; read ahead 138 us for both passes
                                                   // of 8 x 16384 x 256 fp32, in their own turn 145)
   const int32_t *ids = a.ids[r] + t * k + sub;
@@ -772,8 +804,9 @@ cudaError_t run(const GateJob &job, GateParams &a, cudaStream_t s) {
   if (job.tokens <= (uint64_t)kWarps * TPW && job.p <= 2)
     return launch_kernel(rc_gate_one_kernel<T, LPT, VPL>, dim3(1), dim3(kNT), 0, s, a);
   a.blocks = blocks_per_rank(job.tokens, kWarps * TPW, job.p, device_sm_count() * 2);
-  if ((err = launch_kernel(rc_gate_kernel<T, LPT, VPL>, dim3(a.blocks, job.p), dim3(kNT), 0, s, a)) != cudaSuccess)
-    return err;
+  auto kern = rc_gate_kernel<T, LPT, VPL, by_keys(LPT, kMaxK)>;
+  if (!by_keys(LPT, job.top_k)) kern = rc_gate_kernel<T, LPT, VPL, by_keys(LPT, 1)>;
+  if ((err = launch_kernel(kern, dim3(a.blocks, job.p), dim3(kNT), 0, s, a)) != cudaSuccess) return err;
   int span = 1;
   while (span * kStatBlocks < job.experts) span *= 2;
   return launch_kernel(rc_gate_stats_kernel, dim3(kStatBlocks), dim3(kStatNT), 0, s, a, span);

@@ -165,7 +165,7 @@ def test_neighbours_that_differ_in_the_last_bits(rc, e, k, sign):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("e,k", [(64, 8), (100, 8), (128, 16), (200, 8), (256, 16), (512, 16)])
+@pytest.mark.parametrize("e,k", [(20, 16), (30, 4), (64, 8), (64, 16), (100, 8), (128, 16), (200, 8), (256, 16), (512, 16)])
 def test_best_experts_are_neighbours(rc, dt, e, k):
     """The k best in a run of k neighbours (at any offset), in any order, and by halves in two runs."""
     t = 48
@@ -231,7 +231,7 @@ def test_masked_tokens(rc, kind):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("e,k", [(12, 4), (100, 6), (256, 16), (400, 4)])
+@pytest.mark.parametrize("e,k", [(12, 4), (24, 5), (60, 8), (100, 6), (256, 16), (400, 4)])
 def test_minus_infinity_and_non_finite_logits(rc, dt, e, k):
     z = make(1, 8, e, dt, seed=9)[0]
     z[1] = -math.inf                     # an empty row
