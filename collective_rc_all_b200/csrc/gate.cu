@@ -641,8 +641,8 @@ __global__ void __cluster_dims__(kStatBlocks, 1, 1) __launch_bounds__(kStatNT)
 // dz of one token: with a_e = dloss * coef * E * f_e / M, S = the chosen
 // experts' probabilities, and q_i = p_i / S (normalised) or p_i:
 //   dz = p (a - sum p a) + [chosen] q dw - (normalised: [chosen] q, else p) * sum_i q_i dw_i
-// Blocks per SM that the registers are cut to: 8 x 16384 x 256 fp32 67 us with the
-// compiler's own 72 registers and three blocks, 59 us with four; with 8 lanes the
+// Blocks per SM that the registers are cut to: 8 x 16384 x 256 fp32 65 us with the
+// compiler's own 72 registers and three blocks, 57 us with four; with 8 lanes the
 // two slots ahead take more registers than a fourth block is worth (71, 73 us for
 // both passes of 8 x 16384 x 64), with 16 values one block more spills (158, 205
 // us for both passes of 8 x 8192 x 512).
