@@ -15,8 +15,6 @@ carrying the library's message.
 from __future__ import annotations
 
 import ctypes
-import math
-import operator
 import os
 import struct
 from typing import Optional, Sequence, Union
@@ -163,24 +161,33 @@ def _torch_mod():
 
 
 def _is_tensor(x) -> bool:
-    return hasattr(x, "data_ptr") and hasattr(x, "dtype")
+    return (_torch is not None and type(x) is _torch.Tensor) or (hasattr(x, "data_ptr") and hasattr(x, "dtype"))
+
+
+_code_of = {}
+
+
+def _codes():
+    """The library's dtype codes by torch dtype."""
+    if not _code_of:
+        torch = _torch_mod()
+        _code_of.update({torch.float32: FP32, torch.bfloat16: BF16, torch.int32: INT32})
+    return _code_of
 
 
 def _dt(dtype, like=None) -> int:
     if dtype is None:
         if like is None or not _is_tensor(like):
             raise ValueError("dtype is required when buffers are raw addresses")
-        torch = _torch_mod()
-        m = {torch.float32: FP32, torch.bfloat16: BF16, torch.int32: INT32}
-        if like.dtype not in m:
+        code = _codes().get(like.dtype)
+        if code is None:
             raise TypeError(f"unsupported tensor dtype {like.dtype}")
-        return m[like.dtype]
+        return code
     if isinstance(dtype, str):
         return _DT_NAMES[dtype.lower()]
     if isinstance(dtype, int):
         return dtype
-    torch = _torch_mod()
-    return {torch.float32: FP32, torch.bfloat16: BF16, torch.int32: INT32}[dtype]
+    return _codes()[dtype]
 
 
 def _op(op) -> int:
@@ -474,26 +481,20 @@ def _typed(x, dtype, shape, what: str) -> Optional[int]:
     return x.data_ptr()
 
 
-_dtype_of = operator.attrgetter("dtype")
-
-
 def _typed_ptrs(xs, dtype, shape, what: str, counts=None):
     """A pointer array (as bytes) of _typed addresses of one shape, or of
-    [counts[r], *shape[1:]] for each.  Tensors after the first pass on their
-    type, element count and contiguity, checked for all at once."""
+    [counts[r], *shape[1:]] for each."""
     if xs is None:
         return None
-    p = len(xs)
-    if p > 1 and dtype:
-        t, rest = _torch_mod().Tensor, xs[1:]
-        if list(map(type, rest)).count(t) == p - 1 and list(map(_dtype_of, rest)).count(dtype[0]) == p - 1 and \
-                all(map(t.is_contiguous, rest)):
-            n = list(map(t.numel, rest))
-            if n.count(math.prod(shape)) == p - 1 if counts is None else n == [c * shape[1] for c in counts[1:]]:
-                first = shape if counts is None else (counts[0], *shape[1:])
-                return struct.pack(f"{p}Q", _typed(xs[0], dtype, first, what), *map(t.data_ptr, rest))
-    shapes = [shape] * p if counts is None else [(c, *shape[1:]) for c in counts]
-    return struct.pack(f"{p}Q", *[_typed(x, dtype, s, what) for x, s in zip(xs, shapes)])
+    tensor, first, at = _torch_mod().Tensor, dtype[0] if dtype else None, []
+    for r, x in enumerate(xs):
+        if counts is not None:
+            shape = (counts[r], *shape[1:])
+        if type(x) is tensor and x.dtype is first and x.shape == shape and x.is_contiguous():
+            at.append(x.data_ptr())
+        else:
+            at.append(_typed(x, dtype, shape, what))
+    return struct.pack(f"{len(at)}Q", *at)
 
 
 _kinds = None
@@ -530,14 +531,15 @@ def _flat_ptrs(xs, dtype, count: int, what: str):
     """A pointer array (as bytes) of flat buffers of at least `count` elements."""
     if xs is None:
         return None
-    p, t = len(xs), _torch_mod().Tensor
-    if list(map(type, xs)).count(t) == p and list(map(_dtype_of, xs)).count(dtype[0] if dtype else None) == p and \
-            min(map(t.numel, xs)) >= count and all(map(t.is_contiguous, xs)):
-        return struct.pack(f"{p}Q", *map(t.data_ptr, xs))
+    tensor, first, at = _torch_mod().Tensor, dtype[0] if dtype else None, []
     for x in xs:
+        if type(x) is tensor and x.dtype is first and x.numel() >= count and x.is_contiguous():
+            at.append(x.data_ptr())
+            continue
         if _is_tensor(x) and (x.dtype not in dtype or x.numel() < count):
             raise ValueError(f"{what} holds {x.numel()} elements of {x.dtype}; {count} of {dtype} are needed")
-    return struct.pack(f"{p}Q", *map(_addr, xs))
+        at.append(_addr(x))
+    return struct.pack(f"{len(at)}Q", *at)
 
 
 def _dropout_buffers(send, recv, residual, n, dtype):

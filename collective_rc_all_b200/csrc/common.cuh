@@ -29,8 +29,8 @@ constexpr int kMaxRanks = 16;
 // still need.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // pdl_release(): lets the dependents' blocks start where there is room, up to
-// their pdl_wait(), once every block has called it; for kernels whose blocks
-// are all resident at once (no later wave to take room from).
+// their pdl_wait(), once every block has called it or ended; for short kernels
+// in a chain, most of them with all blocks resident at once.
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------- type traits

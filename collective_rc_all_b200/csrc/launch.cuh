@@ -11,9 +11,8 @@
 // with an ordinary launch; only the launch itself and the kernel's prologue
 // (index arithmetic, shared-memory set-up) overlap the previous kernel's
 // drain.  Kernels release their dependents as their blocks exit, except those
-// of the cross entropy, whose blocks are all resident at once and which are a
-// chain of short launches: those release them before their last work
-// (pdl_release()).  Stream capture turns the attribute into programmatic graph
+// of the cross entropy, which are a chain of short launches: those release them
+// before their last work (pdl_release()).  Stream capture turns the attribute into programmatic graph
 // edges.
 //
 // Measured on the sequence of seven collectives captured in one graph
