@@ -201,6 +201,38 @@ def test_padding_may_hold_anything(rc, bad):
     assert torch.equal(a.dh, b.dh) and all(torch.equal(x, y) for x, y in zip(a.dw, b.dw))
 
 
+@pytest.mark.parametrize("tokens,d", [(12, 40), (20, 65), (150, 65), (300, 130)])
+def test_padding_of_few_tokens_and_odd_widths(rc, tokens, d):
+    a, b = Case(tokens, d, 600, 2, seed=4, ignored=0.3), Case(tokens, d, 600, 2, seed=4, ignored=0.3)
+    skip = b.y == b.ignore
+    assert bool(skip.any()) and not bool(skip.all())
+    b.h[skip] = math.nan
+    b.dloss[skip] = math.nan
+    for c in (a, b):
+        c.forward(rc)
+        c.backward(rc)
+    rc.rc_stream_status()
+    assert torch.equal(a.loss, b.loss) and torch.equal(a.dh, b.dh) and all(torch.equal(x, y) for x, y in zip(a.dw, b.dw))
+
+
+@pytest.mark.parametrize("tokens", [5, 8, 11, 16, 17])
+def test_after_a_call_full_of_nan(rc, tokens):
+    """Nothing that an earlier call left in shared memory reaches a tile with few rows."""
+    other = Case(300, 256, 4000, 4, seed=6)
+    other.h.fill_(math.nan)
+    for x in other.w:
+        x.fill_(math.nan)
+    c = Case(tokens, 256, 4000, 4, seed=7)
+    for _ in range(3):
+        other.forward(rc)
+        other.backward(rc)
+        c.forward(rc)
+        c.backward(rc)
+    rc.rc_stream_status()
+    c.check()
+    c.untouched()
+
+
 def test_ignore_index_inside_the_vocabulary(rc):
     c = Case(140, 48, 333, 2, seed=4, ignored=0.2, ignore=5)
     c.forward(rc)
